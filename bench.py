@@ -107,7 +107,7 @@ KERNEL_SOURCES = ("wtconv_kernels.cuh", "wtconv_kinst.cuh", "wtconv_plan.h", "wt
 MEASURED_TRAFFIC = {
     # (workload, call): (bytes per launch, kernel, source digest, profile)
     ("stage1", "bwd_w"): (79442176.0, "wtconv_bwdw_partial_kernel",
-                          "3955a401d12ac3da446d06c2d26f646631dd5e28b326d479e49c854035394e2e",
+                          "e56de9a329b11ff1774ddc61f2ae5b0193e2cf6322440330291aab5bf2427993",
                           "profiles/wtconv_bwdw_partial_kernel_stage1.md"),
 }
 

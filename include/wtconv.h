@@ -26,7 +26,8 @@
  * coordinates (nothing but y is written), and the per-channel and
  * per-subband scales are folded into the conv weights before the convs run.
  *
- * Conventions for every entry point:
+ * Conventions for every entry point of the layer (the map operators at the end
+ * of this file, which stand next to the layer, state theirs there):
  *   - Layouts.  Activations are NCHW or NHWC (desc->layout), contiguous,
  *     stored as float32 or bf16 (desc->dtype); arithmetic is float32; x, dy,
  *     y and dx of one call share the layout.  Parameters and gradients are
@@ -84,7 +85,9 @@ typedef enum {
     WTCONV_ERR_WORKSPACE = 7,   /* workspace missing or smaller than wtconv_workspace_bytes() */
     WTCONV_ERR_UNSUPPORTED = 8, /* valid shape whose plane (or strip) does not fit on chip */
     WTCONV_ERR_CUDA = 9,        /* a CUDA runtime call or kernel launch failed */
-    WTCONV_ERR_LAYOUT = 10      /* unknown activation layout */
+    WTCONV_ERR_LAYOUT = 10,     /* unknown activation layout */
+    WTCONV_ERR_ARGUMENT = 11    /* map operators: eps, dropout, group or 8-bit type out of range, buffers that overlap,
+                                 * or an argument that the others do not allow */
 } wtconv_status_t;
 
 typedef enum { WTCONV_F32 = 0, WTCONV_BF16 = 1 } wtconv_dtype_t; /* activation storage */
@@ -219,6 +222,100 @@ wtconv_status_t wtconv_backward_weight_noalloc(const wtconv_desc_t *d, const voi
                                                const float *wt_w, const float *wt_scale,
                                                float *d_base_w, float *d_base_b, float *d_base_scale,
                                                float *d_wt_w, float *d_wt_scale, wtconv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Map operators: what a network puts around the layer.  The branch's dropout,
+ * its addition to the residual stream, and the root-mean-square norm over the
+ * channels of each pixel, for training and, with an 8-bit output, for serving.
+ *
+ * A map is B x C x H x W in either layout (a matrix of N rows of C values is
+ * the map B = N, H = W = 1).  Its rows are its pixels n = (b*H + h)*W + w.
+ * Conventions (where they differ from the layer's):
+ *   - Any B >= 0 (0: nothing to do, dweight is zeroed), C, H, W > 0; no
+ *     multiple is asked for.  Offsets are 64-bit.  H*W <= 2^30, C <= 2^24.
+ *   - Activations are contiguous, in desc->dtype; they are aligned to their
+ *     element.  (Where the pointers are 16-byte aligned and the adjacent
+ *     extent, C for NHWC and H*W for NCHW, is whole 16-byte chunks, the
+ *     kernels use 16-byte accesses.)
+ *   - Outputs overlap neither an input nor another output (WTCONV_ERR_ARGUMENT).
+ *   - Results do not depend on the order in which CTAs run: repeated calls
+ *     return the same bits.
+ *   - Arithmetic is float32.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int B, C, H, W;
+    int dtype;  /* a wtconv_dtype_t value */
+    int layout; /* a wtconv_layout_t value */
+} wtconv_map_desc_t;
+
+/* What one random decision covers: an element, a channel of a sample, or a
+ * whole sample (stochastic depth). */
+typedef enum { WTCONV_DROP_ELEMENT = 0, WTCONV_DROP_CHANNEL = 1, WTCONV_DROP_SAMPLE = 2 } wtconv_drop_mode_t;
+
+/* Dropout whose mask is never stored.  The random words are Philox4x32-10
+ * (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3",
+ * 2011) with key = seed and
+ *   counter = (c / 4, r mod 2^32, r / 2^32, (offset + *offset_dev) mod 2^32),
+ * r the row (ELEMENT) or the sample b (CHANNEL; SAMPLE with c = 0).  Channel c
+ * takes word c mod 4 and is dropped where it is below floor(p * 2^32).  So the
+ * mask depends on neither layout nor type.  A dropped element counts as 0,
+ * whatever it holds; the others grow by the float32 number next to 1/(1-p). */
+typedef struct {
+    double p;                   /* 0 <= p < 1 */
+    int mode;                   /* a wtconv_drop_mode_t value */
+    unsigned long long seed;
+    unsigned long long offset;  /* the step: another mask for each */
+    const long long *offset_dev; /* NULL, or a device counter that the kernel adds to offset (8-byte aligned): the
+                                  * replays of a captured graph draw new masks as it moves on */
+} wtconv_drop_t;
+
+/* y = residual + d * x in desc->dtype, d the dropout's factors (the product and
+ * the sum rounded once to float32).  residual may be NULL.  The gradients: the
+ * residual's is dy, x's is this call on dy without a residual. */
+wtconv_status_t wtconv_dropout(const wtconv_map_desc_t *d, const wtconv_drop_t *drop, const void *x,
+                               const void *residual, void *y, wtconv_stream_t stream);
+
+/* h = residual + d * x in desc->dtype, rstd[n] = 1 / sqrt(mean over c of h^2 +
+ * eps), y = h * rstd * weight[c] in desc->dtype.  The norm is of h as it is
+ * stored.  residual NULL: h is x, the h argument is NULL and drop must be NULL;
+ * else h is written too.  drop may be NULL (d = 1).  weight: float32 [C].
+ * rstd: float32, one a row, or NULL.  0 < eps < infinity. */
+wtconv_status_t wtconv_rms_norm_forward(const wtconv_map_desc_t *d, float eps, const void *x, const void *residual,
+                                        const wtconv_drop_t *drop, const float *weight, void *y, void *h,
+                                        float *rstd, wtconv_stream_t stream);
+
+/* Gradients of wtconv_rms_norm_forward from its h (x without a residual) and
+ * rstd, with g = dy * weight:
+ *   dres = rstd * (g - h * rstd^2 * mean over c of (g * h)) + dh,
+ *   dx   = d * the same (before its rounding),
+ *   dweight[c] = sum over the rows of dy * h * rstd   (overwritten).
+ * dh: the gradient that reaches h itself, or NULL.  Any of dres, dx, dweight
+ * may be NULL, not all; dx only with drop (without it, it equals dres; with it,
+ * pass the forward's).  workspace: device, 16-byte aligned, at least
+ * wtconv_rms_norm_workspace_bytes(d) bytes where dweight is asked for. */
+wtconv_status_t wtconv_rms_norm_backward(const wtconv_map_desc_t *d, const void *h, const void *dy, const void *dh,
+                                         const wtconv_drop_t *drop, const float *weight, const float *rstd,
+                                         void *dres, void *dx, float *dweight, void *workspace,
+                                         size_t workspace_bytes, wtconv_stream_t stream);
+
+/* Bytes of device workspace for wtconv_rms_norm_backward on the current device
+ * (0 if `d` is invalid or B is 0). */
+size_t wtconv_rms_norm_workspace_bytes(const wtconv_map_desc_t *d);
+
+/* 8-bit outputs: e4m3 (4 exponent bits, largest 448) or whole numbers -127..127. */
+typedef enum { WTCONV_E4M3 = 0, WTCONV_I8 = 1 } wtconv_q8_t;
+
+/* wtconv_rms_norm_forward with an 8-bit output.  v = h * rstd * weight stays in
+ * float32; each group of `group` adjacent channels of a row (32, 64 or 128, the
+ * last may be short; 0: all C) has
+ *   scale = max(max |v| / top, 2^-126),  q = v / scale to nearest, ties to even, top = 448 or 127;
+ * a NaN or infinity in h makes every scale and q of its row what the formulas
+ * give (a NaN scale's e4m3 are NaN, its whole numbers 0).
+ * q: one byte an element in x's layout.  scale: float32, a B x groups x H x W
+ * map in x's layout.  residual and h as above. */
+wtconv_status_t wtconv_rms_norm_q8(const wtconv_map_desc_t *d, float eps, const void *x, const void *residual,
+                                   const float *weight, int q8, int group, void *q, float *scale, void *h,
+                                   wtconv_stream_t stream);
 
 #ifdef __cplusplus
 }

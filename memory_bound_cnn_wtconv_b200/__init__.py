@@ -34,6 +34,7 @@ STATUS = {
     0: "WTCONV_OK", 1: "WTCONV_ERR_NULLPTR", 2: "WTCONV_ERR_BAD_SHAPE", 3: "WTCONV_ERR_BAD_K",
     4: "WTCONV_ERR_BAD_L", 5: "WTCONV_ERR_MISALIGNED", 6: "WTCONV_ERR_DTYPE", 7: "WTCONV_ERR_WORKSPACE",
     8: "WTCONV_ERR_UNSUPPORTED", 9: "WTCONV_ERR_CUDA", 10: "WTCONV_ERR_LAYOUT",
+    11: "WTCONV_ERR_ARGUMENT",
 }
 F32, BF16 = 0, 1
 NCHW, NHWC = 0, 1
@@ -283,3 +284,9 @@ def backward(x, dy, base_w, base_b, base_scale, wt_w, wt_scale, L: int, dx=None,
 from .module import WTConv2d, WTConvFunction, wtconv  # noqa: E402
 
 __all__ += ["WTConv2d", "WTConvFunction", "wtconv"]
+
+# What stands around the layer: dropout and the RMS norm (the same way).
+from . import maps as _maps  # noqa: E402
+from .maps import *  # noqa: E402,F401,F403
+
+__all__ += _maps.__all__

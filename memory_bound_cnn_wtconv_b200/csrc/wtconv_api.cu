@@ -76,6 +76,7 @@ const char* wtconv_status_string(wtconv_status_t s) {
         case WTCONV_ERR_UNSUPPORTED: return "plane too large to stage on chip";
         case WTCONV_ERR_CUDA: return "CUDA runtime error";
         case WTCONV_ERR_LAYOUT: return "unknown activation layout (0 = NCHW, 1 = NHWC)";
+        case WTCONV_ERR_ARGUMENT: return "argument out of range, overlapping buffers, or not allowed with the others";
     }
     return "unknown status";
 }

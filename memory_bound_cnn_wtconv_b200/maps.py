@@ -1,0 +1,475 @@
+"""Map operators next to the layer: dropout and the RMS norm over channels.
+
+``rms_norm`` and ``dropout`` are the autograd forms, ``RMSNorm2d`` and
+``BranchDropout`` the modules; the ``*_forward`` / ``*_backward`` / ``*_q8``
+calls marshal arguments for the C ABI in ``include/wtconv.h``, which has the
+formulas.  Activations are [B, C, H, W] maps, contiguous (NCHW) or
+channels-last contiguous (NHWC), or contiguous [N, C] rows, in float32 or
+bfloat16 on one CUDA device; the activations of a call share shape, layout and
+type.  Any size is taken, odd ones and B = 0 too.
+
+A call runs on ``stream`` if given (what it allocates then belongs to that
+stream), else on the current stream of the activations' device.  Everything
+runs in the CUDA kernels of ``libwtconv_b200.so``; there is no CPU fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import BF16, F32, NCHW, NHWC, _check, load_library
+
+__all__ = [
+    "Drop", "dropout_forward", "dropout_backward", "rms_norm_forward", "rms_norm_backward", "rms_norm_q8",
+    "rms_norm_workspace_bytes", "dropout", "rms_norm", "DropoutFunction", "RMSNormFunction", "RMSNorm2d",
+    "BranchDropout",
+]
+
+_MODES = {"element": 0, "channel": 1, "sample": 2}
+_Q8 = {torch.float8_e4m3fn: 0, torch.int8: 1}
+_M64 = (1 << 64) - 1
+
+
+class MapDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("C", ctypes.c_int), ("H", ctypes.c_int), ("W", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+class _DropArgs(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("mode", ctypes.c_int), ("seed", ctypes.c_ulonglong),
+                ("offset", ctypes.c_ulonglong), ("offset_dev", ctypes.c_void_p)]
+
+
+class Drop:
+    """One call's dropout: probability ``p`` (0 <= p < 1), what a decision
+    covers (``mode``: "element", "channel" of a sample, or "sample"), and the
+    counter that names the mask: the same ``seed`` and ``offset`` give the same
+    mask, in both layouts and types and in the backward.
+
+    ``offset`` is a number (of the step, say), or an int64 CUDA tensor of one
+    element, which the kernels read when they run: a captured graph that moves
+    it on between replays draws a new mask in each.  Do not change it between a
+    forward and its backward (the autograd forms raise if it was).
+    """
+
+    __slots__ = ("p", "mode", "seed", "offset", "_args")
+
+    def __init__(self, p: float, mode: str = "element", seed: int = 0, offset=0):
+        p = float(p)
+        if not 0.0 <= p < 1.0:
+            raise ValueError(f"p must be at least 0 and below 1, got {p}")
+        if mode not in _MODES:
+            raise ValueError(f"mode must be one of {sorted(_MODES)}, got {mode!r}")
+        self.p, self.mode, self.seed, self.offset = p, mode, int(seed), offset
+        dev = None
+        if isinstance(offset, torch.Tensor):
+            if offset.dtype != torch.int64 or offset.numel() != 1 or not offset.is_cuda:
+                raise ValueError("an offset tensor must be an int64 CUDA tensor of one element")
+            dev, offset = offset.data_ptr(), 0
+        self._args = _DropArgs(p, _MODES[mode], self.seed & _M64, int(offset) & _M64, dev)
+
+    def __repr__(self) -> str:
+        return f"Drop(p={self.p}, mode={self.mode!r}, seed={self.seed}, offset={self.offset})"
+
+
+_fns = None
+
+
+def _lib():
+    """The library's map operators, with their argument types."""
+    global _fns
+    if _fns is None:
+        lib = load_library()
+        vp, dp, ap, f, i, sz = (ctypes.c_void_p, ctypes.POINTER(MapDesc), ctypes.POINTER(_DropArgs), ctypes.c_float,
+                                ctypes.c_int, ctypes.c_size_t)
+        lib.wtconv_dropout.argtypes = [dp, ap, vp, vp, vp, vp]
+        lib.wtconv_rms_norm_forward.argtypes = [dp, f, vp, vp, ap, vp, vp, vp, vp, vp]
+        lib.wtconv_rms_norm_q8.argtypes = [dp, f, vp, vp, vp, i, i, vp, vp, vp, vp]
+        lib.wtconv_rms_norm_backward.argtypes = [dp, vp, vp, vp, ap, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.wtconv_rms_norm_workspace_bytes.argtypes = [dp]
+        lib.wtconv_rms_norm_workspace_bytes.restype = sz
+        for name in ("wtconv_dropout", "wtconv_rms_norm_forward", "wtconv_rms_norm_q8", "wtconv_rms_norm_backward"):
+            getattr(lib, name).restype = i
+        _fns = lib
+    return _fns
+
+
+def _desc(x: torch.Tensor, name: str) -> MapDesc:
+    """The map that a tensor is; raises for what is none."""
+    if x.dtype is torch.float32:
+        dtype = F32
+    elif x.dtype is torch.bfloat16:
+        dtype = BF16
+    else:
+        raise TypeError(f"activations must be float32 or bfloat16, got {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape = x.shape
+    if len(shape) == 4:
+        if x.is_contiguous():
+            layout = NCHW
+        elif x.is_contiguous(memory_format=torch.channels_last):
+            layout = NHWC
+        else:
+            raise ValueError(f"{name} must be contiguous (NCHW) or channels-last contiguous (NHWC)")
+        B, C, H, W = shape
+    elif len(shape) == 2:
+        if not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        B, C = shape
+        H = W = 1
+        layout = NHWC
+    else:
+        raise ValueError(f"{name} must be a [B, C, H, W] map or [N, C] rows, got {len(shape)} dimensions")
+    if not (C > 0 and H > 0 and W > 0):
+        raise ValueError(f"{name} has no channels or no pixels: {tuple(shape)}")
+    return MapDesc(B, C, H, W, dtype, layout)
+
+
+def _like(t: torch.Tensor, name: str, x: torch.Tensor, layout: int, dtype=None) -> int:
+    """The address of an activation that has to be as x is."""
+    if t.dtype is not (dtype or x.dtype) or t.shape != x.shape or t.device != x.device:
+        raise ValueError(f"{name} must have the shape {tuple(x.shape)}, type {dtype or x.dtype} and device of the input")
+    if not (t.is_contiguous() if layout == NCHW or t.dim() == 2
+            else t.is_contiguous(memory_format=torch.channels_last)):
+        raise ValueError(f"{name} must have the layout of the input ({'NHWC' if layout == NHWC else 'NCHW'})")
+    return t.data_ptr()
+
+
+def _vector(t: torch.Tensor, name: str, x: torch.Tensor, shape) -> int:
+    if t.dtype is not torch.float32 or t.device != x.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor on {x.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _drop_ref(drop, x):
+    if drop is None:
+        return None
+    if not isinstance(drop, Drop):
+        raise TypeError(f"drop must be a Drop, got {type(drop).__name__}")
+    if isinstance(drop.offset, torch.Tensor) and drop.offset.device != x.device:
+        raise ValueError(f"the offset tensor is on {drop.offset.device}, the activations on {x.device}")
+    return ctypes.byref(drop._args)
+
+
+def _rows_shape(x: torch.Tensor):
+    return (x.shape[0],) if x.dim() == 2 else (x.shape[0], x.shape[2], x.shape[3])
+
+
+def _on(x, stream, call):
+    """Run ``call`` with the stream, and the device of x, as the current ones."""
+    if stream is not None:
+        if stream.device != x.device:
+            raise ValueError(f"the stream is on {stream.device}, the activations on {x.device}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    index = x.device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return call(torch.cuda.current_stream(index).cuda_stream)
+    return call(torch.cuda.current_stream(index).cuda_stream)
+
+
+def dropout_forward(x, drop: Drop, residual=None, y=None, stream=None):
+    """y = residual + drop(x) via ``wtconv_dropout``; returns y (allocated if
+    not given)."""
+    lib = _lib()
+    d = _desc(x, "x")
+    if drop is None:
+        raise TypeError("drop must be a Drop")
+    ref = _drop_ref(drop, x)
+    rp = _like(residual, "residual", x, d.layout) if residual is not None else None
+
+    def call(s):
+        out = torch.empty_like(x) if y is None else y
+        _check(lib.wtconv_dropout(ctypes.byref(d), ref, x.data_ptr(), rp, _like(out, "y", x, d.layout), s),
+               "wtconv_dropout")
+        return out
+    return _on(x, stream, call)
+
+
+def dropout_backward(dy, drop: Drop, dx=None, stream=None):
+    """The gradient of x, drop(dy) with the forward's mask (the residual's is
+    dy); returns dx."""
+    return dropout_forward(dy, drop, None, dx, stream)
+
+
+def rms_norm_forward(x, weight, residual=None, drop: Drop = None, eps: float = 1e-6, y=None, h=None, rstd=None,
+                     stream=None):
+    """h = residual + drop(x), y = h / rms(h) * weight via
+    ``wtconv_rms_norm_forward``; returns (y, h, rstd).  Without a residual h is
+    x itself.  ``rstd=False`` leaves rstd out (inference): None is returned."""
+    lib = _lib()
+    d = _desc(x, "x")
+    wp = _vector(weight, "weight", x, (d.C,))
+    ref = _drop_ref(drop, x)
+    rp = _like(residual, "residual", x, d.layout) if residual is not None else None
+    if residual is None and h is not None:
+        raise ValueError("without a residual, h is x: give none")
+
+    def call(s):
+        oy = torch.empty_like(x) if y is None else y
+        oh, hp = x, None
+        if residual is not None:
+            oh = torch.empty_like(x) if h is None else h
+            hp = _like(oh, "h", x, d.layout)
+        if rstd is False:
+            r, rsp = None, None
+        else:
+            r = torch.empty(_rows_shape(x), dtype=torch.float32, device=x.device) if rstd is None else rstd
+            rsp = _vector(r, "rstd", x, _rows_shape(x))
+        _check(lib.wtconv_rms_norm_forward(ctypes.byref(d), eps, x.data_ptr(), rp, ref, wp,
+                                           _like(oy, "y", x, d.layout), hp, rsp, s), "wtconv_rms_norm_forward")
+        return oy, oh, r
+    return _on(x, stream, call)
+
+
+def rms_norm_workspace_bytes(x: torch.Tensor) -> int:
+    """Workspace of ``rms_norm_backward`` for activations like x."""
+    d = _desc(x, "x")
+    return _on(x, None, lambda s: int(_lib().wtconv_rms_norm_workspace_bytes(ctypes.byref(d))))
+
+
+def rms_norm_backward(h, dy, weight, rstd, dh=None, drop: Drop = None, dx=None, dresidual=None, dweight=None,
+                      workspace=None, stream=None):
+    """Gradients of ``rms_norm_forward`` from its h and rstd, via
+    ``wtconv_rms_norm_backward``; ``dh`` is the gradient that reaches h itself.
+    Returns (dx, dresidual, dweight).  Without ``drop`` (which has to be the
+    forward's) the two activations' gradients are the same tensor.
+    ``dresidual=False`` or ``dweight=False`` leaves that gradient out (None is
+    returned for it); ``dx=False`` too, with ``drop`` only.  ``workspace`` is a uint8 CUDA tensor of
+    at least ``rms_norm_workspace_bytes`` bytes; allocated here if not given."""
+    lib = _lib()
+    d = _desc(h, "h")
+    dyp = _like(dy, "dy", h, d.layout)
+    wp = _vector(weight, "weight", h, (d.C,))
+    rsp = _vector(rstd, "rstd", h, _rows_shape(h))
+    dhp = _like(dh, "dh", h, d.layout) if dh is not None else None
+    ref = _drop_ref(drop, h)
+    if drop is None:
+        if dx is not None and dx is not False and dresidual is not None and dresidual is not False and dx is not dresidual:
+            raise ValueError("without dropout dx and dresidual are the same: give one")
+        skip = dx is False or dresidual is False
+        same = (dx if dx is not None else dresidual) if not skip else False
+
+    def call(s):
+        if drop is None:
+            r = None if same is False else torch.empty_like(h) if same is None else same
+            g, gp = r, None
+        else:
+            r = None if dresidual is False else torch.empty_like(h) if dresidual is None else dresidual
+            g = None if dx is False else torch.empty_like(h) if dx is None else dx
+            gp = None if g is None else _like(g, "dx", h, d.layout)
+        rp = None if r is None else _like(r, "dresidual", h, d.layout)
+        w = ws = wwp = wsp = None
+        nbytes = 0
+        if dweight is not False:
+            w = torch.empty((d.C,), dtype=torch.float32, device=h.device) if dweight is None else dweight
+            wwp = _vector(w, "dweight", h, (d.C,))
+            if workspace is None:
+                nbytes = lib.wtconv_rms_norm_workspace_bytes(ctypes.byref(d))
+                if nbytes:
+                    ws = torch.empty((nbytes,), dtype=torch.uint8, device=h.device)
+                    wsp = ws.data_ptr()
+            else:
+                if not workspace.is_cuda or workspace.device != h.device or not workspace.is_contiguous():
+                    raise ValueError(f"workspace must be a contiguous tensor on {h.device}")
+                wsp, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        if rp is not None or gp is not None or wwp is not None:
+            _check(lib.wtconv_rms_norm_backward(ctypes.byref(d), h.data_ptr(), dyp, dhp, ref, wp, rsp, rp, gp, wwp,
+                                                wsp, nbytes, s), "wtconv_rms_norm_backward")
+        return g, r, w
+    return _on(h, stream, call)
+
+
+def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, dtype=torch.float8_e4m3fn, group: int = 0, q=None,
+                scale=None, h=None, stream=None):
+    """``rms_norm_forward`` with an 8-bit output (``torch.float8_e4m3fn`` or
+    ``torch.int8``) and one float32 scale for each ``group`` adjacent channels
+    of a pixel (32, 64, 128, or 0: all), via ``wtconv_rms_norm_q8``; q * scale
+    stands for the norm.  Returns (q, scale, h): scale is [B, groups, H, W] (or
+    [N, groups]) in the layout of x; h is x without a residual."""
+    lib = _lib()
+    if dtype not in _Q8:
+        raise TypeError(f"dtype must be torch.float8_e4m3fn or torch.int8, got {dtype}")
+    if group not in (0, 32, 64, 128):
+        raise ValueError(f"group must be 0, 32, 64 or 128, got {group}")
+    d = _desc(x, "x")
+    wp = _vector(weight, "weight", x, (d.C,))
+    rp = _like(residual, "residual", x, d.layout) if residual is not None else None
+    if residual is None and h is not None:
+        raise ValueError("without a residual, h is x: give none")
+    groups = -(-d.C // group) if group else 1
+    sshape = (x.shape[0], groups, *x.shape[2:])
+    fmt = torch.channels_last if d.layout == NHWC and x.dim() == 4 else torch.contiguous_format
+
+    def call(s):
+        oq = torch.empty_like(x, dtype=dtype) if q is None else q
+        qp = _like(oq, "q", x, d.layout, dtype)
+        sc = torch.empty(sshape, dtype=torch.float32, device=x.device, memory_format=fmt) if scale is None else scale
+        if sc.dtype is not torch.float32 or tuple(sc.shape) != sshape or sc.device != x.device \
+                or not sc.is_contiguous(memory_format=fmt):
+            raise ValueError(f"scale must be a float32 tensor of shape {sshape} in the layout of x on {x.device}")
+        oh, hp = x, None
+        if residual is not None:
+            oh = torch.empty_like(x) if h is None else h
+            hp = _like(oh, "h", x, d.layout)
+        _check(lib.wtconv_rms_norm_q8(ctypes.byref(d), eps, x.data_ptr(), rp, wp, _Q8[dtype], group, qp,
+                                      sc.data_ptr(), hp, s), "wtconv_rms_norm_q8")
+        return oq, sc, oh
+    return _on(x, stream, call)
+
+
+def _laid_out(x):
+    """x in one of the kernels' layouts (channels-last maps stay NHWC)."""
+    return x if x.dim() == 4 and x.is_contiguous(memory_format=torch.channels_last) else x.contiguous()
+
+
+def _as(t, x):
+    """t in the layout of x."""
+    if t is None:
+        return None
+    return t.contiguous(memory_format=torch.contiguous_format if x.is_contiguous() else torch.channels_last)
+
+
+def _saved_offset(drop):
+    """The offset tensor, for autograd's check that nothing changed it."""
+    return drop.offset if drop is not None and isinstance(drop.offset, torch.Tensor) else None
+
+
+class DropoutFunction(torch.autograd.Function):
+    """y = residual + drop(x).  The backward computes the mask again; nothing of
+    the size of x is saved."""
+
+    @staticmethod
+    def forward(ctx, x, residual, drop: Drop):
+        x = _laid_out(x)
+        ctx.drop = drop
+        ctx.save_for_backward(_saved_offset(drop))
+        ctx.like = x.is_contiguous(), x.dtype
+        return dropout_forward(x, drop, _as(residual, x))
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        ctx.saved_tensors  # raises where the offset tensor has changed
+        need = ctx.needs_input_grad
+        dx = None
+        if need[0]:
+            fmt = torch.contiguous_format if ctx.like[0] else torch.channels_last
+            dx = dropout_backward(dy.to(ctx.like[1]).contiguous(memory_format=fmt), ctx.drop)
+        return dx, dy if need[1] else None, None
+
+
+class RMSNormFunction(torch.autograd.Function):
+    """(y, h) of ``rms_norm_forward``.  Saves h (x without a residual) and one
+    float a pixel."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, drop: Drop, eps: float):
+        x = _laid_out(x)
+        y, h, rstd = rms_norm_forward(x, weight, _as(residual, x), drop, eps)
+        ctx.save_for_backward(h, weight, rstd, _saved_offset(drop))
+        ctx.drop = drop
+        ctx.set_materialize_grads(False)
+        return (y, h) if residual is not None else y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd, _ = ctx.saved_tensors
+        need, drop = ctx.needs_input_grad, ctx.drop
+        if dy is None and dh is None:
+            return (None,) * 5
+        dy = torch.zeros_like(h) if dy is None else _as(dy.to(h.dtype), h)
+        if drop is None:
+            dx = None if need[0] or need[2] else False
+            dres = None
+        else:
+            dx, dres = (None if need[0] else False), (None if need[2] else False)
+        dx, dres, dw = rms_norm_backward(h, dy, weight, rstd,
+                                         None if dh is None else _as(dh.to(h.dtype), h), drop, dx, dres,
+                                         None if need[1] else False)
+        return dx if need[0] else None, dw, dres if need[2] else None, None, None
+
+
+def dropout(x, drop: Drop, residual=None):
+    """residual + drop(x) with autograd support."""
+    return DropoutFunction.apply(x, residual, drop)
+
+
+def rms_norm(x, weight, residual=None, drop: Drop = None, eps: float = 1e-6):
+    """The norm of x over its channels, with autograd support; with a residual
+    the pair (norm of residual + drop(x), that sum)."""
+    return RMSNormFunction.apply(x, weight, residual, drop, eps)
+
+
+class RMSNorm2d(torch.nn.Module):
+    """RMS norm over the channels of a map (or of [N, C] rows), with a float32
+    weight [C].  ``forward(x)`` is the norm; ``forward(x, residual, drop)`` is
+    the pair (norm of residual + drop(x), that sum), in one pass."""
+
+    def __init__(self, channels: int, eps: float = 1e-6, device=None):
+        super().__init__()
+        self.channels, self.eps = int(channels), float(eps)
+        self.weight = torch.nn.Parameter(torch.ones((self.channels,), dtype=torch.float32, device=device))
+
+    def forward(self, x, residual=None, drop: Drop = None):
+        return RMSNormFunction.apply(x, self.weight, residual, drop, self.eps)
+
+    def extra_repr(self) -> str:
+        return f"channels={self.channels}, eps={self.eps}"
+
+
+class BranchDropout(torch.nn.Module):
+    """Dropout of a branch: ``forward(x, residual)`` is residual + drop(x) in
+    training, and plainly residual + x in evaluation.
+
+    ``seed`` names the module's masks (drawn from torch's CPU generator if not
+    given, so processes that seed it alike draw alike); each training call takes
+    the next step as its offset.  ``next_drop()`` is that call's ``Drop``, for a
+    fused norm.  With ``capturable`` the step is a CUDA tensor which the calls
+    move on, so every replay of a captured graph draws new masks.  Seed and
+    step are part of the state dict.
+    """
+
+    def __init__(self, p: float, mode: str = "element", seed: int = None, capturable: bool = False, device=None):
+        super().__init__()
+        Drop(p, mode)  # raises for what is out of range
+        self.p, self.mode, self.capturable = float(p), mode, bool(capturable)
+        self.seed = int(torch.randint(1 << 62, (1,))) if seed is None else int(seed)
+        self.steps = 0
+        if self.capturable:
+            self.register_buffer("step", torch.zeros((1,), dtype=torch.int64, device=device))
+
+    def get_extra_state(self):
+        return {"seed": self.seed, "steps": self.steps}
+
+    def set_extra_state(self, state):
+        self.seed, self.steps = int(state["seed"]), int(state["steps"])
+
+    def next_drop(self):
+        """The ``Drop`` of one training call; None where nothing is dropped."""
+        if not self.training or self.p == 0.0:
+            return None
+        if self.capturable:
+            offset = self.step.clone()  # the call's own: the counter may move on before its backward
+            self.step.add_(1)
+        else:
+            offset = self.steps
+            self.steps += 1
+        return Drop(self.p, self.mode, self.seed, offset)
+
+    def forward(self, x, residual=None):
+        drop = self.next_drop()
+        if drop is None:
+            if residual is None:
+                return x
+            drop = Drop(0.0, self.mode)
+        return DropoutFunction.apply(x, residual, drop)
+
+    def extra_repr(self) -> str:
+        return f"p={self.p}, mode={self.mode!r}, capturable={self.capturable}"
