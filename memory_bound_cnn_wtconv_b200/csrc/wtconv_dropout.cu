@@ -1,40 +1,166 @@
 // Counter-based dropout of a map: y = residual + d * x, d = 0 or the float
 // next to 1 / (1 - p).  The mask is a function of (seed, offset, row,
 // channel) alone, so it is never stored: the backward is the same kernel on dy.
+//
+// Bound by memory: x (and the residual) read once, y written once.  A random
+// quad covers four channels of a pixel, and each kernel gives a thread all of
+// what it draws:
+//   rows    channels adjacent: a 16-byte chunk of channels (one or two quads);
+//   planes  pixels adjacent: a 16-byte chunk of pixels of four channels (one
+//           quad a pixel), or single pixels where planes are not whole chunks;
+//   spans   whole stretches of memory under one decision (samples in either
+//           layout, channels of NCHW): x is not read where it is dropped.
+#include <algorithm>
+
 #include "wtconv_map_launch.h"
 
 namespace wtc {
 
-template <typename T>
-__global__ void wtconv_dropout_kernel(MapShape m, DropArgs a, MapDrop d) {
-    const long long n = m.rows * m.C, step = (long long)gridDim.x * blockDim.x;
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int N>
+__device__ __forceinline__ void drop_values(float (&f)[N], const float (&r)[N], uint32_t keep, float grown) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = keep >> e & 1 ? __fmaf_rn(f[e], grown, r[e]) : r[e];
+}
+
+template <typename T, bool RES>
+__global__ void __launch_bounds__(kThreads) wtconv_dropout_rows_kernel(MapShape m, DropArgs a, MapDrop d, int vec) {
+    constexpr int V = kVec<T>;
+    const int slots = (m.C + V - 1) / V;
+    const long long n = m.rows * slots, step = (long long)gridDim.x * kThreads;
     const uint32_t offset = drop_offset(d);
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
-        long long row;
-        int c;
-        if (m.nhwc) {
-            row = i / m.C;
-            c = (int)(i - row * m.C);
-        } else {
-            const long long plane = i / m.HW, b = plane / m.C;
-            c = (int)(plane - b * m.C);
-            row = b * m.HW + (i - plane * m.HW);
-        }
-        const bool keep = keep_quad(d, offset, drop_row(d, m, row), d.mode == WTCONV_DROP_SAMPLE ? 0 : c >> 2) >> (c & 3) & 1;
-        const float r = a.residual ? to_f(static_cast<const T*>(a.residual)[i]) : 0.0f;
-        const float v = to_f(static_cast<const T*>(a.x)[i]);
-        static_cast<T*>(a.y)[i] = from_f<T>(keep ? __fmaf_rn(v, d.grown, r) : r);
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+        const long long row = n <= 0xffffffffLL ? (uint32_t)i / (uint32_t)slots : i / slots;
+        const int c = (int)(i - row * slots) * V;
+        const long long base = row * m.C;
+        uint4 x = load_channels(static_cast<const T*>(a.x) + base, c, m.C, vec), res;
+        if (RES) res = load_channels(static_cast<const T*>(a.residual) + base, c, m.C, vec);
+        const long long drow = d.mode == WTCONV_DROP_ELEMENT ? row : drop_row(d, m, row);
+        uint32_t keep = keep_quad(d, offset, drow, c >> 2);
+        if (V == 8) keep |= keep_quad(d, offset, drow, (c >> 2) + 1) << 4;
+        float f[V], r[V] = {};
+        unpack(x, f);
+        if (RES) unpack(res, r);
+        drop_values(f, r, keep, d.grown);
+        store_channels(static_cast<T*>(a.y) + base, c, m.C, vec, pack(f));
     }
 }
 
+// A block of threads lies along the pixels of a quad's planes.
+template <typename T, int VP, bool RES>
+__global__ void __launch_bounds__(kThreads) wtconv_dropout_planes_kernel(MapShape m, DropArgs a, MapDrop d) {
+    using R = typename Chunk<T, VP>::type;
+    const int quads = (m.C + 3) / 4, chunks = m.HW / VP;
+    const long long n = m.rows / m.HW * quads * chunks, step = (long long)gridDim.x * kThreads;
+    const uint32_t offset = drop_offset(d);
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+        const long long bq = n <= 0xffffffffLL ? (uint32_t)i / (uint32_t)chunks : i / chunks;
+        const int p = (int)(i - bq * chunks) * VP;
+        const long long b = bq / quads;
+        const int quad = (int)(bq - b * quads);
+        const long long base = (b * m.C + 4 * quad) * m.HW + p;
+        const T* x = static_cast<const T*>(a.x) + base;
+        const T* res = static_cast<const T*>(a.residual) + base;
+        R rx[4], rr[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (4 * quad + j < m.C) {
+                rx[j] = *reinterpret_cast<const R*>(x + (long long)j * m.HW);
+                if (RES) rr[j] = *reinterpret_cast<const R*>(res + (long long)j * m.HW);
+            }
+        uint32_t keep[4] = {};  // bit v: pixel v
+#pragma unroll
+        for (int v = 0; v < VP; ++v) {
+            const uint32_t k = keep_quad(d, offset, b * m.HW + p + v, quad);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) keep[j] |= (k >> j & 1) << v;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (4 * quad + j < m.C) {
+                float f[VP], r[VP] = {};
+                unpack(rx[j], f);
+                if (RES) unpack(rr[j], r);
+                drop_values(f, r, keep[j], d.grown);
+                *reinterpret_cast<R*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = Chunk<T, VP>::from(f);
+            }
+    }
+}
+
+// Spans of `len` adjacent elements, each under one decision; blockIdx.y walks
+// the spans and blockIdx.x shares one out.  All three pointers are equally far
+// from a 16-byte boundary where vec is set.
+template <typename T, bool RES>
+__global__ void __launch_bounds__(kThreads) wtconv_dropout_spans_kernel(MapShape m, DropArgs a, MapDrop d, long long spans, long long len, int vec) {
+    constexpr int V = kVec<T>;
+    const uint32_t offset = drop_offset(d);
+    for (long long k = blockIdx.y; k < spans; k += gridDim.y) {
+        bool keep;
+        if (d.mode == WTCONV_DROP_SAMPLE) {
+            keep = keep_quad(d, offset, k, 0);
+        } else {
+            const long long b = k / m.C;
+            const int c = (int)(k - b * m.C);
+            keep = keep_quad(d, offset, b, c >> 2) >> (c & 3) & 1;
+        }
+        const T* x = static_cast<const T*>(a.x) + k * len;
+        const T* res = static_cast<const T*>(a.residual) + k * len;
+        T* y = static_cast<T*>(a.y) + k * len;
+        auto one = [&](long long i) {
+            const float r = RES ? to_f(res[i]) : 0.0f;
+            y[i] = from_f<T>(keep ? __fmaf_rn(to_f(x[i]), d.grown, r) : r);
+        };
+        const long long head = vec ? min(len, (long long)((16 - (uintptr_t)y % 16) % 16 / sizeof(T))) : len;
+        const long long body = (len - head) / V, first = (long long)blockIdx.x * kThreads + threadIdx.x;
+        const long long step = (long long)gridDim.x * kThreads;
+        const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+        const uint4* rv = reinterpret_cast<const uint4*>(res + head);
+        uint4* yv = reinterpret_cast<uint4*>(y + head);
+#pragma unroll 4
+        for (long long i = first; i < body; i += step) {
+            float f[V] = {}, r[V] = {};
+            if (RES) unpack(rv[i], r);
+            if (keep) unpack(xv[i], f);
+            drop_values(f, r, keep ? 0xffu : 0u, d.grown);
+            yv[i] = pack(f);
+        }
+        for (long long i = first; i < head; i += step) one(i);
+        for (long long i = head + body * V + first; i < len; i += step) one(i);
+    }
+}
+
+template <typename T, bool RES>
+void run(const MapShape& m, const DropArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
+    constexpr int V = kVec<T>;
+    const uintptr_t ax = (uintptr_t)a.x % 16, ar = (uintptr_t)a.residual % 16, ay = (uintptr_t)a.y % 16;
+    const bool whole = !ax && !ar && !ay;
+    auto ctas = [&](long long threads) { return (unsigned)std::min((threads + kThreads - 1) / kThreads, 64LL * sms); };
+    if (d.mode == WTCONV_DROP_SAMPLE || (d.mode == WTCONV_DROP_CHANNEL && !m.nhwc) || !d.on) {
+        // Nothing dropped: one span, kept by any decision (the threshold is 0).
+        const bool sample = d.mode == WTCONV_DROP_SAMPLE;
+        const long long spans = !d.on ? 1 : m.rows / m.HW * (sample ? 1 : m.C), len = m.rows * m.C / spans;
+        const bool vec = ax == ay && (!RES || ar == ay);
+        const unsigned across = (unsigned)std::min((len / V + kThreads) / kThreads, std::max(1LL, 32LL * sms / spans));
+        const dim3 grid(across, (unsigned)std::min(spans, std::max(1LL, 32LL * sms / across)));
+        wtconv_dropout_spans_kernel<T, RES><<<grid, kThreads, 0, s>>>(m, a, d, spans, len, vec);
+    } else if (m.nhwc) {
+        const bool vec = m.C % V == 0 && whole;
+        wtconv_dropout_rows_kernel<T, RES><<<ctas(m.rows * ((m.C + V - 1) / V)), kThreads, 0, s>>>(m, a, d, vec);
+    } else {
+        const long long quads = m.rows / m.HW * ((m.C + 3) / 4);
+        if (m.HW % V == 0 && whole) wtconv_dropout_planes_kernel<T, V, RES><<<ctas(quads * (m.HW / V)), kThreads, 0, s>>>(m, a, d);
+        else wtconv_dropout_planes_kernel<T, 1, RES><<<ctas(quads * m.HW), kThreads, 0, s>>>(m, a, d);
+    }
+}
+
+}  // namespace
+
 cudaError_t launch_dropout(const MapShape& m, int dtype, const DropArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
-    const int threads = 256;
-    const long long blocks = (m.rows * m.C + threads - 1) / threads;
-    const unsigned grid = (unsigned)(blocks < 16LL * sms ? blocks : 16LL * sms);
-    if (dtype == WTCONV_F32)
-        wtconv_dropout_kernel<float><<<grid, threads, 0, s>>>(m, a, d);
-    else
-        wtconv_dropout_kernel<__nv_bfloat16><<<grid, threads, 0, s>>>(m, a, d);
+    if (dtype == WTCONV_F32) a.residual ? run<float, true>(m, a, d, sms, s) : run<float, false>(m, a, d, sms, s);
+    else a.residual ? run<__nv_bfloat16, true>(m, a, d, sms, s) : run<__nv_bfloat16, false>(m, a, d, sms, s);
     return cudaGetLastError();
 }
 

@@ -39,6 +39,72 @@ __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Sixteen stored bytes and the V = 16 / sizeof(T) floats they hold.
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ void unpack(const uint4& r, float (&f)[4]) {
+    f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y), f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void unpack(const uint4& r, float (&f)[8]) {
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(u[i] << 16), f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// One stored value (pixels whose planes are not whole 16-byte chunks).
+__device__ __forceinline__ void unpack(float r, float (&f)[1]) { f[0] = r; }
+__device__ __forceinline__ void unpack(__nv_bfloat16 r, float (&f)[1]) { f[0] = __bfloat162float(r); }
+
+// N stored values as one register group: uint4 for a 16-byte chunk, T for one value.
+template <typename T, int N>
+struct Chunk {
+    using type = uint4;
+    static __device__ __forceinline__ uint4 zero() { return make_uint4(0, 0, 0, 0); }
+    static __device__ __forceinline__ uint4 from(const float (&f)[N]) { return pack(f); }
+};
+template <typename T>
+struct Chunk<T, 1> {
+    using type = T;
+    static __device__ __forceinline__ T zero() { return from_f<T>(0.0f); }
+    static __device__ __forceinline__ T from(const float (&f)[1]) { return from_f<T>(f[0]); }
+};
+
+// The chunk of channels c .. c + V - 1 of a row at p (16 bytes at once with
+// vec; else one by one, channels past C as zeros).
+template <typename T>
+__device__ __forceinline__ uint4 load_channels(const T* p, int c, int C, bool vec) {
+    if (vec) return *reinterpret_cast<const uint4*>(p + c);
+    float f[kVec<T>];
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e) f[e] = c + e < C ? to_f(p[c + e]) : 0.0f;
+    return pack(f);
+}
+template <typename T>
+__device__ __forceinline__ void store_channels(T* p, int c, int C, bool vec, const uint4& r) {
+    if (vec) {
+        *reinterpret_cast<uint4*>(p + c) = r;
+        return;
+    }
+    float f[kVec<T>];
+    unpack(r, f);
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e)
+        if (c + e < C) p[c + e] = from_f<T>(f[e]);
+}
+
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as
 // easy as 1, 2, 3", 2011): four random words from a 128-bit counter and a
 // 64-bit key.

@@ -1,0 +1,53 @@
+// What the two layouts' RMS norm kernels share (the formulas: wtconv_norm.cu).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "wtconv_map_launch.h"
+
+namespace wtc {
+
+// CTAs per SM of the weight gradient's partial sums, at most (the workspace
+// holds one vector of C floats for each).
+constexpr int kNormParts = 8;
+
+inline long long norm_parts(const MapShape& m, int sms) { return std::min(m.rows, (long long)kNormParts * sms); }
+
+// How JOIN reads h: x itself, residual + x, or residual + dropout of x.
+enum { kPlain = 0, kResidual = 1, kDropped = 2 };
+
+// The scale of a group whose largest |v| has these bits, and its inverse's
+// place: q = v / scale.
+__device__ __forceinline__ float q8_scale(uint32_t bits, int q8) {
+    const float s = __uint_as_float(bits) / (q8 == WTCONV_E4M3 ? 448.0f : 127.0f);
+    return s < 1.17549435e-38f ? 1.17549435e-38f : s;  // a NaN stays
+}
+
+// Four values to four bytes.
+__device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d, int q8) {
+    if (q8 == WTCONV_E4M3) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+        return lo | hi << 16;
+    }
+    const float f[4] = {a, b, c, d};
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int v = isnan(f[i]) ? 0 : max(-127, min(127, __float2int_rn(f[i])));
+        r |= (uint32_t)(v & 255) << (8 * i);
+    }
+    return r;
+}
+
+// |v| as bits that are ordered like |v|, NaN above infinity.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+cudaError_t launch_norm_rows_fwd(const MapShape& m, int dtype, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s);
+cudaError_t launch_norm_rows_bwd(const MapShape& m, int dtype, const NormBwdArgs& a, const MapDrop& d, int sms, int* parts, cudaStream_t s);
+cudaError_t launch_norm_planes_fwd(const MapShape& m, int dtype, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s);
+cudaError_t launch_norm_planes_bwd(const MapShape& m, int dtype, const NormBwdArgs& a, const MapDrop& d, int sms, int* parts, cudaStream_t s);
+
+}  // namespace wtc
