@@ -19,48 +19,45 @@ namespace wtc {
 namespace {
 
 constexpr int kThreads = 256;
-
-template <int N>
-__device__ __forceinline__ void drop_values(float (&f)[N], const float (&r)[N], uint32_t keep, float grown) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) f[e] = keep >> e & 1 ? __fmaf_rn(f[e], grown, r[e]) : r[e];
-}
+// Shorter stretches under one decision go to the rows and planes kernels.
+constexpr long long kLeastSpan = 2048;
 
 template <typename T, bool RES>
-__global__ void __launch_bounds__(kThreads) wtconv_dropout_rows_kernel(MapShape m, DropArgs a, MapDrop d, int vec) {
+__global__ void __launch_bounds__(kThreads) wtconv_dropout_rows_kernel(MapShape m, DropArgs a, MapDrop d, Divide by_slots, Divide by_hw, int vec) {
     constexpr int V = kVec<T>;
-    const int slots = (m.C + V - 1) / V;
+    const int slots = (int)by_slots.d;
     const long long n = m.rows * slots, step = (long long)gridDim.x * kThreads;
     const uint32_t offset = drop_offset(d);
     for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-        const long long row = n <= 0xffffffffLL ? (uint32_t)i / (uint32_t)slots : i / slots;
+        const long long row = by_slots(i);
         const int c = (int)(i - row * slots) * V;
         const long long base = row * m.C;
-        uint4 x = load_channels(static_cast<const T*>(a.x) + base, c, m.C, vec), res;
+        const uint4 x = load_channels(static_cast<const T*>(a.x) + base, c, m.C, vec);
+        uint4 res = make_uint4(0, 0, 0, 0);
         if (RES) res = load_channels(static_cast<const T*>(a.residual) + base, c, m.C, vec);
-        const long long drow = d.mode == WTCONV_DROP_ELEMENT ? row : drop_row(d, m, row);
-        uint32_t keep = keep_quad(d, offset, drow, c >> 2);
-        if (V == 8) keep |= keep_quad(d, offset, drow, (c >> 2) + 1) << 4;
-        float f[V], r[V] = {};
+        const long long drow = d.mode == WTCONV_DROP_ELEMENT ? row : by_hw(row);
+        float f[V], r[V];
         unpack(x, f);
-        if (RES) unpack(res, r);
-        drop_values(f, r, keep, d.grown);
-        store_channels(static_cast<T*>(a.y) + base, c, m.C, vec, pack(f));
+        unpack(res, r);
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+            uint4 u = drop_words(d, offset, drow, d.mode == WTCONV_DROP_SAMPLE ? 0 : (c + e) >> 2);
+            if (d.mode == WTCONV_DROP_SAMPLE) u = make_uint4(u.x, u.x, u.x, u.x);
+            drop_add4(d, u, f + e, r + e);
+        }
+        store_channels(static_cast<T*>(a.y) + base, c, m.C, vec, pack(r));
     }
 }
 
-// A block of threads lies along the pixels of a quad's planes.
 template <typename T, int VP, bool RES>
-__global__ void __launch_bounds__(kThreads) wtconv_dropout_planes_kernel(MapShape m, DropArgs a, MapDrop d) {
+__global__ void __launch_bounds__(kThreads) wtconv_dropout_planes_kernel(MapShape m, DropArgs a, MapDrop d, Divide by_chunks, Divide by_quads) {
     using R = typename Chunk<T, VP>::type;
-    const int quads = (m.C + 3) / 4, chunks = m.HW / VP;
-    const long long n = m.rows / m.HW * quads * chunks, step = (long long)gridDim.x * kThreads;
+    const int quads = (int)by_quads.d, chunks = (int)by_chunks.d;
+    const long long n = m.rows / VP * quads, step = (long long)gridDim.x * kThreads;
     const uint32_t offset = drop_offset(d);
     for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-        const long long bq = n <= 0xffffffffLL ? (uint32_t)i / (uint32_t)chunks : i / chunks;
-        const int p = (int)(i - bq * chunks) * VP;
-        const long long b = bq / quads;
-        const int quad = (int)(bq - b * quads);
+        const long long bq = by_chunks(i), b = by_quads(bq);
+        const int p = (int)(i - bq * chunks) * VP, quad = (int)(bq - b * quads);
         const long long base = (b * m.C + 4 * quad) * m.HW + p;
         const T* x = static_cast<const T*>(a.x) + base;
         const T* res = static_cast<const T*>(a.residual) + base;
@@ -72,11 +69,22 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_planes_kernel(MapShap
                 if (RES) rr[j] = *reinterpret_cast<const R*>(res + (long long)j * m.HW);
             }
         uint32_t keep[4] = {};  // bit v: pixel v
+        if (d.mode == WTCONV_DROP_ELEMENT) {
 #pragma unroll
-        for (int v = 0; v < VP; ++v) {
-            const uint32_t k = keep_quad(d, offset, b * m.HW + p + v, quad);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) keep[j] |= (k >> j & 1) << v;
+            for (int v = 0; v < VP; ++v) {
+                const uint4 u = drop_words(d, offset, b * m.HW + p + v, quad);
+                keep[0] |= u.x >= d.thresh ? 1u << v : 0u;
+                keep[1] |= u.y >= d.thresh ? 1u << v : 0u;
+                keep[2] |= u.z >= d.thresh ? 1u << v : 0u;
+                keep[3] |= u.w >= d.thresh ? 1u << v : 0u;
+            }
+        } else {
+            const bool sample = d.mode == WTCONV_DROP_SAMPLE;
+            const uint4 u = drop_words(d, offset, b, sample ? 0 : quad);
+            keep[0] = u.x >= d.thresh ? ~0u : 0u;
+            keep[1] = (sample ? u.x : u.y) >= d.thresh ? ~0u : 0u;
+            keep[2] = (sample ? u.x : u.z) >= d.thresh ? ~0u : 0u;
+            keep[3] = (sample ? u.x : u.w) >= d.thresh ? ~0u : 0u;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -84,8 +92,10 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_planes_kernel(MapShap
                 float f[VP], r[VP] = {};
                 unpack(rx[j], f);
                 if (RES) unpack(rr[j], r);
-                drop_values(f, r, keep[j], d.grown);
-                *reinterpret_cast<R*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = Chunk<T, VP>::from(f);
+#pragma unroll
+                for (int e = 0; e < VP; ++e)
+                    if (keep[j] >> e & 1) r[e] = __fmaf_rn(f[e], d.grown, r[e]);
+                *reinterpret_cast<R*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = Chunk<T, VP>::from(r);
             }
     }
 }
@@ -99,12 +109,12 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_spans_kernel(MapShape
     const uint32_t offset = drop_offset(d);
     for (long long k = blockIdx.y; k < spans; k += gridDim.y) {
         bool keep;
-        if (d.mode == WTCONV_DROP_SAMPLE) {
-            keep = keep_quad(d, offset, k, 0);
+        if (d.mode == WTCONV_DROP_SAMPLE || !d.on) {
+            keep = keep_sample(d, offset, k);
         } else {
             const long long b = k / m.C;
             const int c = (int)(k - b * m.C);
-            keep = keep_quad(d, offset, b, c >> 2) >> (c & 3) & 1;
+            keep = keep_bits(d, drop_words(d, offset, b, c >> 2)) >> (c & 3) & 1;
         }
         const T* x = static_cast<const T*>(a.x) + k * len;
         const T* res = static_cast<const T*>(a.residual) + k * len;
@@ -124,8 +134,11 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_spans_kernel(MapShape
             float f[V] = {}, r[V] = {};
             if (RES) unpack(rv[i], r);
             if (keep) unpack(xv[i], f);
-            drop_values(f, r, keep ? 0xffu : 0u, d.grown);
-            yv[i] = pack(f);
+            if (keep) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) r[e] = __fmaf_rn(f[e], d.grown, r[e]);
+            }
+            yv[i] = pack(r);
         }
         for (long long i = first; i < head; i += step) one(i);
         for (long long i = head + body * V + first; i < len; i += step) one(i);
@@ -138,21 +151,29 @@ void run(const MapShape& m, const DropArgs& a, const MapDrop& d, int sms, cudaSt
     const uintptr_t ax = (uintptr_t)a.x % 16, ar = (uintptr_t)a.residual % 16, ay = (uintptr_t)a.y % 16;
     const bool whole = !ax && !ar && !ay;
     auto ctas = [&](long long threads) { return (unsigned)std::min((threads + kThreads - 1) / kThreads, 64LL * sms); };
-    if (d.mode == WTCONV_DROP_SAMPLE || (d.mode == WTCONV_DROP_CHANNEL && !m.nhwc) || !d.on) {
-        // Nothing dropped: one span, kept by any decision (the threshold is 0).
-        const bool sample = d.mode == WTCONV_DROP_SAMPLE;
-        const long long spans = !d.on ? 1 : m.rows / m.HW * (sample ? 1 : m.C), len = m.rows * m.C / spans;
+    // Nothing dropped: one span, kept by any decision (the threshold is 0).
+    const bool sample = d.mode == WTCONV_DROP_SAMPLE;
+    const long long samples = m.rows / m.HW, spans = !d.on ? 1 : samples * (sample ? 1 : m.C), len = m.rows * m.C / spans;
+    const bool stretches = !d.on || sample || (d.mode == WTCONV_DROP_CHANNEL && !m.nhwc);
+    if (stretches && len >= kLeastSpan) {
         const bool vec = ax == ay && (!RES || ar == ay);
         const unsigned across = (unsigned)std::min((len / V + kThreads) / kThreads, std::max(1LL, 32LL * sms / spans));
         const dim3 grid(across, (unsigned)std::min(spans, std::max(1LL, 32LL * sms / across)));
         wtconv_dropout_spans_kernel<T, RES><<<grid, kThreads, 0, s>>>(m, a, d, spans, len, vec);
     } else if (m.nhwc) {
         const bool vec = m.C % V == 0 && whole;
-        wtconv_dropout_rows_kernel<T, RES><<<ctas(m.rows * ((m.C + V - 1) / V)), kThreads, 0, s>>>(m, a, d, vec);
+        const int slots = (m.C + V - 1) / V;
+        wtconv_dropout_rows_kernel<T, RES><<<ctas(m.rows * slots), kThreads, 0, s>>>(
+            m, a, d, divide_by(slots, m.rows * slots), divide_by(m.HW, m.rows), vec);
     } else {
-        const long long quads = m.rows / m.HW * ((m.C + 3) / 4);
-        if (m.HW % V == 0 && whole) wtconv_dropout_planes_kernel<T, V, RES><<<ctas(quads * (m.HW / V)), kThreads, 0, s>>>(m, a, d);
-        else wtconv_dropout_planes_kernel<T, 1, RES><<<ctas(quads * m.HW), kThreads, 0, s>>>(m, a, d);
+        const int quads = (m.C + 3) / 4;
+        const Divide by_quads = divide_by(quads, samples * quads);
+        if (m.HW % V == 0 && whole)
+            wtconv_dropout_planes_kernel<T, V, RES><<<ctas(m.rows / V * quads), kThreads, 0, s>>>(
+                m, a, d, divide_by(m.HW / V, m.rows / V * quads), by_quads);
+        else
+            wtconv_dropout_planes_kernel<T, 1, RES><<<ctas(m.rows * quads), kThreads, 0, s>>>(
+                m, a, d, divide_by(m.HW, m.rows * quads), by_quads);
     }
 }
 

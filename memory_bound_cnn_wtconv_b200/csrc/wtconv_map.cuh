@@ -10,6 +10,7 @@
 #include <stdint.h>
 
 #include "../../include/wtconv.h"
+#include "wtconv_plan.h"
 
 namespace wtc {
 
@@ -23,7 +24,7 @@ struct MapShape {
 struct MapDrop {
     uint32_t thresh;                // dropped where the random word is below this
     float grown;                    // factor of what stays: the float next to 1 / (1 - p)
-    uint32_t k0, k1;                // Philox key: the seed
+    uint32_t key[20];               // Philox's round keys, two a round (kernel parameters: free operands)
     uint32_t offset;
     const long long* offset_dev;    // added to offset if not NULL (read by the kernel: a replayed graph sees its value)
     int mode;                       // wtconv_drop_mode_t
@@ -107,19 +108,23 @@ __device__ __forceinline__ void store_channels(T* p, int c, int C, bool vec, con
 
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as
 // easy as 1, 2, 3", 2011): four random words from a 128-bit counter and a
-// 64-bit key.
-__device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1) {
+// 64-bit key, whose ten round keys come ready made.
+__device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, const uint32_t (&key)[20]) {
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ key[2 * r];
         c1 = (uint32_t)b;
-        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ key[2 * r + 1];
         c3 = (uint32_t)a;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
     return make_uint4(c0, c1, c2, c3);
+}
+inline void philox_keys(unsigned long long seed, uint32_t (&key)[20]) {
+    for (uint32_t r = 0; r < 10; ++r) {
+        key[2 * r] = (uint32_t)seed + r * 0x9E3779B9u;
+        key[2 * r + 1] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
+    }
 }
 
 __device__ __forceinline__ uint32_t drop_offset(const MapDrop& d) {
@@ -131,12 +136,42 @@ __device__ __forceinline__ long long drop_row(const MapDrop& d, const MapShape& 
     return d.mode == WTCONV_DROP_ELEMENT ? n : n / m.HW;
 }
 
-// Keep bits (bit j: channel 4 * quad + j) of one mask row.
-__device__ __forceinline__ uint32_t keep_quad(const MapDrop& d, uint32_t offset, long long row, uint32_t quad) {
-    const uint4 u = philox(quad, (uint32_t)row, (uint32_t)((unsigned long long)row >> 32), offset, d.k0, d.k1);
-    if (d.mode == WTCONV_DROP_SAMPLE) return u.x >= d.thresh ? 15u : 0u;
+// The random words of channels 4 * quad .. 4 * quad + 3 of one mask row.
+__device__ __forceinline__ uint4 drop_words(const MapDrop& d, uint32_t offset, long long row, uint32_t quad) {
+    return philox(quad, (uint32_t)row, (uint32_t)((unsigned long long)row >> 32), offset, d.key);
+}
+// A sample's one decision.
+__device__ __forceinline__ bool keep_sample(const MapDrop& d, uint32_t offset, long long b) {
+    return drop_words(d, offset, b, 0).x >= d.thresh;
+}
+// Four keep bits.
+__device__ __forceinline__ uint32_t keep_bits(const MapDrop& d, const uint4& u) {
     return (u.x >= d.thresh ? 1u : 0u) | (u.y >= d.thresh ? 2u : 0u) | (u.z >= d.thresh ? 4u : 0u) |
            (u.w >= d.thresh ? 8u : 0u);
+}
+// r + d * f of four channels, into r.
+__device__ __forceinline__ void drop_add4(const MapDrop& d, const uint4& u, const float* f, float* r) {
+    if (u.x >= d.thresh) r[0] = __fmaf_rn(f[0], d.grown, r[0]);
+    if (u.y >= d.thresh) r[1] = __fmaf_rn(f[1], d.grown, r[1]);
+    if (u.z >= d.thresh) r[2] = __fmaf_rn(f[2], d.grown, r[2]);
+    if (u.w >= d.thresh) r[3] = __fmaf_rn(f[3], d.grown, r[3]);
+}
+
+// n / d of a count: a multiply and a shift below 2^31, else a division.
+struct Divide {
+    FastDiv f;
+    long long d;
+    int small;  // every n is below 2^31
+    __device__ __forceinline__ long long operator()(long long n) const {
+        return small ? (long long)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift) : n / d;
+    }
+};
+inline Divide divide_by(long long d, long long most) {
+    Divide v{};
+    v.d = d;
+    v.small = most < (1LL << 31) && d < (1LL << 31);
+    if (v.small) v.f = make_fastdiv((uint32_t)d);
+    return v;
 }
 
 }  // namespace wtc

@@ -5,6 +5,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "../../include/wtconv.h"
 #include "wtconv_launch.h"
 #include "wtconv_map_launch.h"
@@ -12,6 +14,17 @@
 namespace wtc {
 
 namespace {
+
+// planning_sm_count() of each device, asked once (0: not yet).  A count is
+// written whole and never changes, so calls on several threads agree.
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return planning_sm_count();
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) known[dev].store(n = planning_sm_count(), std::memory_order_relaxed);
+    return n;
+}
 
 wtconv_status_t map_shape(const wtconv_map_desc_t* d, MapShape* m) {
     if (!d) return WTCONV_ERR_NULLPTR;
@@ -37,8 +50,7 @@ wtconv_status_t map_drop(const wtconv_drop_t* p, MapDrop* d) {
     if ((uintptr_t)p->offset_dev % 8) return WTCONV_ERR_MISALIGNED;
     d->thresh = (uint32_t)floor(p->p * 4294967296.0);  // p < 1: at most 2^32 - 1
     d->grown = (float)(1.0 / (1.0 - p->p));
-    d->k0 = (uint32_t)p->seed;
-    d->k1 = (uint32_t)(p->seed >> 32);
+    philox_keys(p->seed, d->key);
     d->offset = (uint32_t)p->offset;
     d->offset_dev = (const long long*)p->offset_dev;
     d->mode = p->mode;
@@ -94,7 +106,7 @@ wtconv_status_t norm_forward(const wtconv_map_desc_t* d, float eps, const void* 
     st = check_spans(sp, 7);
     if (st != WTCONV_OK) return st;
     const NormFwdArgs a{x, residual, weight, y, h, rstd, scale, eps, q8, group};
-    return launch_norm_fwd(m, d->dtype, a, md, planning_sm_count(), (cudaStream_t)stream) == cudaSuccess ? WTCONV_OK
+    return launch_norm_fwd(m, d->dtype, a, md, sm_count(), (cudaStream_t)stream) == cudaSuccess ? WTCONV_OK
                                                                                                     : WTCONV_ERR_CUDA;
 }
 
@@ -122,7 +134,7 @@ wtconv_status_t wtconv_dropout(const wtconv_map_desc_t* d, const wtconv_drop_t* 
     st = check_spans(sp, 3);
     if (st != WTCONV_OK) return st;
     const DropArgs a{x, residual, y};
-    return launch_dropout(m, d->dtype, a, md, planning_sm_count(), (cudaStream_t)stream) == cudaSuccess ? WTCONV_OK
+    return launch_dropout(m, d->dtype, a, md, sm_count(), (cudaStream_t)stream) == cudaSuccess ? WTCONV_OK
                                                                                                    : WTCONV_ERR_CUDA;
 }
 
@@ -146,7 +158,7 @@ wtconv_status_t wtconv_rms_norm_q8(const wtconv_map_desc_t* d, float eps, const 
 size_t wtconv_rms_norm_workspace_bytes(const wtconv_map_desc_t* d) {
     MapShape m;
     if (map_shape(d, &m) != WTCONV_OK || m.rows == 0) return 0;
-    return norm_workspace_floats(m, d->dtype, planning_sm_count()) * sizeof(float);
+    return norm_workspace_floats(m, d->dtype, sm_count()) * sizeof(float);
 }
 
 wtconv_status_t wtconv_rms_norm_backward(const wtconv_map_desc_t* d, const void* h, const void* dy, const void* dh,
@@ -166,7 +178,7 @@ wtconv_status_t wtconv_rms_norm_backward(const wtconv_map_desc_t* d, const void*
         return WTCONV_OK;
     }
     if (!h || !dy || !weight || !rstd || (!dres && !dx && !dweight)) return WTCONV_ERR_NULLPTR;
-    const int sms = planning_sm_count();
+    const int sms = sm_count();
     const size_t need = dweight ? norm_workspace_floats(m, d->dtype, sms) * sizeof(float) : 0;
     if (need && (!workspace || workspace_bytes < need)) return WTCONV_ERR_WORKSPACE;
     const size_t es = esize_of(d), n = (size_t)m.rows * m.C;

@@ -62,12 +62,12 @@ __device__ __forceinline__ uint32_t keep_tile(const MapDrop& d, uint32_t offset,
     if (d.mode == WTCONV_DROP_ELEMENT) {
 #pragma unroll
         for (int v = 0; v < VP; ++v) {
-            const uint32_t k = keep_quad(d, offset, row + v, quad);
+            const uint32_t k = keep_bits(d, drop_words(d, offset, row + v, quad));
 #pragma unroll
             for (int j = 0; j < 4; ++j) bits |= (k >> j & 1) << (j * VP + v);
         }
     } else {
-        const uint32_t k = keep_quad(d, offset, b, quad);
+        const uint32_t k = keep_bits(d, drop_words(d, offset, b, quad));
 #pragma unroll
         for (int j = 0; j < 4; ++j) bits |= k >> j & 1 ? ((1u << VP) - 1) << (j * VP) : 0u;
     }
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
         const T* x = static_cast<const T*>(a.x) + base;
         const T* res = static_cast<const T*>(a.residual) + base;
         T* h = static_cast<T*>(a.h) + base;
-        uint32_t whole = 15;
-        if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) whole = keep_quad(d, offset, b, 0);
+        bool whole = true;
+        if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, b);
         R raw[GR][4], rr[GR][4];
         float ss[VP] = {};
         auto load = [&](int g, R (&rx)[4], R (&rres)[4]) {
@@ -237,14 +237,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
                 float s[VP];
                 if (c0 < m.C) {
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) s[e] = __uint_as_float(top[at * px + pl * VP + e]);
+                    for (int e = 0; e < VP; ++e) s[e] = 1.0f / __uint_as_float(top[at * px + pl * VP + e]);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float f[VP];
                     if (!value(g, j, hraw[j], f)) continue;
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) f[e] /= s[e];
+                    for (int e = 0; e < VP; ++e) f[e] *= s[e];  // one rounding more than v / scale
                     uint8_t* o = q + (long long)(c0 + j) * m.HW;
                     if constexpr (VP == 1) {
                         *o = (uint8_t)q8_pack4(f[0], 0.0f, 0.0f, 0.0f, a.q8);
@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
         const T* h = static_cast<const T*>(a.h) + base;
         const T* dy = static_cast<const T*>(a.dy) + base;
         const T* dh = static_cast<const T*>(a.dh) + base;
-        uint32_t whole = 15;
-        if (DROP && d.mode == WTCONV_DROP_SAMPLE) whole = keep_quad(d, offset, b, 0);
+        bool whole = true;
+        if (DROP && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, b);
         float r[VP] = {};
         if (live) {
 #pragma unroll

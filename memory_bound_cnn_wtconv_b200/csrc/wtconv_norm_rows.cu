@@ -84,14 +84,6 @@ __device__ __forceinline__ void load_weight(const float* w, int c, int C, bool v
     }
 }
 
-// Keep bits of the V channels from c on.
-template <int V>
-__device__ __forceinline__ uint32_t keep_channels(const MapDrop& d, uint32_t offset, long long drow, int c) {
-    uint32_t k = keep_quad(d, offset, drow, c >> 2);
-    if (V == 8) k |= keep_quad(d, offset, drow, (c >> 2) + 1) << 4;
-    return k;
-}
-
 template <typename T, int NV, int JOIN, bool Q8>
 __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, NormFwdArgs a, MapDrop d, int tpr, int vec) {
     constexpr int V = kVec<T>;
@@ -100,6 +92,13 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
     const int t = threadIdx.x % tpr, step = blockDim.x / tpr, slots = (m.C + V - 1) / V;
     const int iters = NV ? NV : (slots + tpr - 1) / tpr;
     const uint32_t offset = JOIN == kDropped ? drop_offset(d) : 0;
+    float wr[NR][V];  // the weights of this thread's channels, for all its rows
+    if (NV) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            if (i * tpr + t < slots) load_weight<V>(a.weight, (i * tpr + t) * V, m.C, vec, wr[i]);
+        }
+    }
     // Every thread of a CTA makes the same number of rounds.
     for (long long row0 = (long long)blockIdx.x * step; row0 < m.rows; row0 += (long long)gridDim.x * step) {
         const long long row = row0 + threadIdx.x / tpr;
@@ -109,10 +108,10 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
         const T* res = static_cast<const T*>(a.residual) + base;
         T* h = static_cast<T*>(a.h) + base;
         long long drow = 0;
-        uint32_t whole = 15;  // a sample's decision
+        bool whole = true;  // a sample's decision
         if (JOIN == kDropped) {
             drow = drop_row(d, m, row);
-            if (d.mode == WTCONV_DROP_SAMPLE) whole = keep_quad(d, offset, drow, 0);
+            if (d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, drow);
         }
         uint4 raw[NR], rr[NR];
         float ss = 0.0f;
@@ -130,16 +129,19 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
             if (JOIN != kPlain) {
                 float r[V];
                 unpack(rres, r);
-                if (JOIN == kDropped) {
-                    uint32_t keep = whole ? 0xffu : 0u;
-                    if (d.mode != WTCONV_DROP_SAMPLE) keep = keep_channels<V>(d, offset, drow, k * V);
+                if (JOIN == kDropped && d.mode != WTCONV_DROP_SAMPLE) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) f[e] = keep >> e & 1 ? __fmaf_rn(f[e], d.grown, r[e]) : r[e];
+                    for (int e = 0; e < V; e += 4) drop_add4(d, drop_words(d, offset, drow, (k * V + e) >> 2), f + e, r + e);
+                } else if (JOIN == kDropped) {
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) r[e] = __fmaf_rn(f[e], d.grown, r[e]);
+                    }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) f[e] += r[e];
+                    for (int e = 0; e < V; ++e) r[e] += f[e];
                 }
-                rx = pack(f);
+                rx = pack(r);
                 if (live && k < slots) store_channels(h, k * V, m.C, vec, rx);
                 unpack(rx, f);  // the norm is of h as it is stored
             }
@@ -161,12 +163,13 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
         auto value = [&](int i, uint4 hraw, float (&f)[V]) {
             const int k = i * tpr + t;
             if (!live || k >= slots) return false;
-            if (!NV) hraw = load_channels(JOIN == kPlain ? x : h, k * V, m.C, vec);  // this thread's own
-            float w[V];
+            if (!NV) {
+                hraw = load_channels(JOIN == kPlain ? x : h, k * V, m.C, vec);  // this thread's own
+                load_weight<V>(a.weight, k * V, m.C, vec, wr[0]);
+            }
             unpack(hraw, f);
-            load_weight<V>(a.weight, k * V, m.C, vec, w);
 #pragma unroll
-            for (int e = 0; e < V; ++e) f[e] = f[e] * r * w[e];
+            for (int e = 0; e < V; ++e) f[e] = f[e] * r * wr[NV ? i : 0][e];
             return true;
         };
         if (!Q8) {
@@ -214,10 +217,11 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
                 }
                 float f[V];
                 if (!value(i, hraw, f)) return;
+                const float inv = 1.0f / scale;  // one rounding more than v / scale, within the rounding to 8 bits
                 uint32_t b[V / 4];
 #pragma unroll
                 for (int e = 0; e < V; e += 4)
-                    b[e / 4] = q8_pack4(f[e] / scale, f[e + 1] / scale, f[e + 2] / scale, f[e + 3] / scale, a.q8);
+                    b[e / 4] = q8_pack4(f[e] * inv, f[e + 1] * inv, f[e + 2] * inv, f[e + 3] * inv, a.q8);
                 uint8_t* q = static_cast<uint8_t*>(a.y) + base;
                 const int c = k * V;
                 if (vec) {
@@ -248,7 +252,13 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
     const int t = threadIdx.x % tpr, step = blockDim.x / tpr, slots = (m.C + V - 1) / V;
     const int iters = NV ? NV : (slots + tpr - 1) / tpr;
     const uint32_t offset = DROP ? drop_offset(d) : 0;
-    float acc[NR][V] = {};
+    float acc[NR][V] = {}, wr[NR][V];  // of this thread's channels, for all its rows
+    if (NV) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            if (i * tpr + t < slots) load_weight<V>(a.weight, (i * tpr + t) * V, m.C, vec, wr[i]);
+        }
+    }
     for (long long row0 = (long long)blockIdx.x * step; row0 < m.rows; row0 += (long long)gridDim.x * step) {
         const long long row = row0 + threadIdx.x / tpr;
         const bool live = row < m.rows;
@@ -258,10 +268,10 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
         const T* dh = static_cast<const T*>(a.dh) + base;
         const float r = live ? a.rstd[row] : 0.0f;
         long long drow = 0;
-        uint32_t whole = 15;
+        bool whole = true;
         if (DROP) {
             drow = drop_row(d, m, row);
-            if (d.mode == WTCONV_DROP_SAMPLE) whole = keep_quad(d, offset, drow, 0);
+            if (d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, drow);
         }
         uint4 hr[NR], gr[NR], er[NR];
         float gh = 0.0f;
@@ -278,10 +288,11 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
         auto dot = [&](int i, const uint4& rh, const uint4& rg, float (&sum)[V]) {
             const int k = i * tpr + t;
             if (k >= slots) return;
-            float fh[V], fg[V], w[V];
+            float fh[V], fg[V];
+            float (&w)[V] = wr[NV ? i : 0];
             unpack(rh, fh);
             unpack(rg, fg);
-            load_weight<V>(a.weight, k * V, m.C, vec, w);
+            if (!NV) load_weight<V>(a.weight, k * V, m.C, vec, w);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float p = fg[e] * fh[e];
@@ -306,20 +317,25 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
             const int k = i * tpr + t, c = k * V;
             if (!live || k >= slots) return;
             if (!NV) load(i, rh, rg), re = load_dh(i);
-            float fh[V], fg[V], fe[V], w[V];
+            float fh[V], fg[V], fe[V];
+            float (&w)[V] = wr[NV ? i : 0];
             unpack(rh, fh);
             unpack(rg, fg);
             unpack(re, fe);
-            load_weight<V>(a.weight, c, m.C, vec, w);
+            if (!NV) load_weight<V>(a.weight, c, m.C, vec, w);
 #pragma unroll
             for (int e = 0; e < V; ++e) fe[e] += r * (fg[e] * w[e] - fh[e] * s);
             if (a.dres) store_channels(static_cast<T*>(a.dres) + base, c, m.C, vec, pack(fe));
             if (DROP && a.dx) {
-                uint32_t keep = whole ? 0xffu : 0u;
-                if (d.mode != WTCONV_DROP_SAMPLE) keep = keep_channels<V>(d, offset, drow, c);
+                float g[V] = {};
+                if (d.mode != WTCONV_DROP_SAMPLE) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) fe[e] = keep >> e & 1 ? fe[e] * d.grown : 0.0f;
-                store_channels(static_cast<T*>(a.dx) + base, c, m.C, vec, pack(fe));
+                    for (int e = 0; e < V; e += 4) drop_add4(d, drop_words(d, offset, drow, (c + e) >> 2), fe + e, g + e);
+                } else if (whole) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) g[e] = fe[e] * d.grown;
+                }
+                store_channels(static_cast<T*>(a.dx) + base, c, m.C, vec, pack(g));
             }
         };
         if (NV) {
@@ -359,6 +375,14 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
     }
 }
 
+// CTAs of a kernel that an SM holds, asked once for each kernel and block size.
+template <typename K>
+int resident(K kernel, int threads, size_t smem) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
+    return n;
+}
+
 bool aligned_to(const void* p, uintptr_t n) { return (uintptr_t)p % n == 0; }
 
 template <typename T, int JOIN, bool Q8>
@@ -370,13 +394,16 @@ void run_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms,
     const int least = Q8 && a.group < m.C ? std::max(4, a.group / V) : 4;
     const RowsGeom g = rows_geom(m, V, vec, least);
     const long long ctas = (m.rows + g.step - 1) / g.step;
-    const unsigned grid = (unsigned)std::min(ctas, 32LL * sms);
+    auto go = [&](auto kernel) {
+        const unsigned grid = (unsigned)std::min(ctas, ctas <= 4LL * sms ? ctas : (long long)resident(kernel, g.threads, 0) * sms);
+        kernel<<<grid, g.threads, 0, s>>>(m, a, d, g.tpr, vec);
+    };
     switch (g.nv) {
-        case 1: wtconv_norm_rows_kernel<T, 1, JOIN, Q8><<<grid, g.threads, 0, s>>>(m, a, d, g.tpr, vec); break;
-        case 2: wtconv_norm_rows_kernel<T, 2, JOIN, Q8><<<grid, g.threads, 0, s>>>(m, a, d, g.tpr, vec); break;
-        case 3: wtconv_norm_rows_kernel<T, 3, JOIN, Q8><<<grid, g.threads, 0, s>>>(m, a, d, g.tpr, vec); break;
-        case 4: wtconv_norm_rows_kernel<T, 4, JOIN, Q8><<<grid, g.threads, 0, s>>>(m, a, d, g.tpr, vec); break;
-        default: wtconv_norm_rows_kernel<T, 0, JOIN, Q8><<<grid, g.threads, 0, s>>>(m, a, d, g.tpr, vec); break;
+        case 1: go(wtconv_norm_rows_kernel<T, 1, JOIN, Q8>); break;
+        case 2: go(wtconv_norm_rows_kernel<T, 2, JOIN, Q8>); break;
+        case 3: go(wtconv_norm_rows_kernel<T, 3, JOIN, Q8>); break;
+        case 4: go(wtconv_norm_rows_kernel<T, 4, JOIN, Q8>); break;
+        default: go(wtconv_norm_rows_kernel<T, 0, JOIN, Q8>); break;
     }
 }
 
@@ -396,18 +423,22 @@ int run_bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, 
                      aligned_to(a.weight, 16) && aligned_to(a.dres, 16) && aligned_to(a.dx, 16);
     const RowsGeom g = rows_geom(m, V, vec, 4);
     const long long ctas = (m.rows + g.step - 1) / g.step;
-    const unsigned grid = (unsigned)std::min(ctas, norm_parts(m, sms));
     const size_t smem = g.tpr <= 32 && g.threads > 32 && a.dweight ? (size_t)(g.threads / 32) * m.C * 4 : 0;
+    const long long most = norm_parts(m, sms);
+    auto go = [&](auto kernel, size_t bytes) {
+        const unsigned grid = (unsigned)std::min(std::min(ctas, most), ctas <= 2LL * sms ? ctas : (long long)resident(kernel, g.threads, bytes) * sms);
+        kernel<<<grid, g.threads, bytes, s>>>(m, a, d, g.tpr, vec);
+        return (int)grid;
+    };
     switch (g.nv) {
-        case 1: wtconv_norm_rows_bwd_kernel<T, 1, DROP><<<grid, g.threads, smem, s>>>(m, a, d, g.tpr, vec); break;
-        case 2: wtconv_norm_rows_bwd_kernel<T, 2, DROP><<<grid, g.threads, smem, s>>>(m, a, d, g.tpr, vec); break;
-        case 3: wtconv_norm_rows_bwd_kernel<T, 3, DROP><<<grid, g.threads, smem, s>>>(m, a, d, g.tpr, vec); break;
-        case 4: wtconv_norm_rows_bwd_kernel<T, 4, DROP><<<grid, g.threads, smem, s>>>(m, a, d, g.tpr, vec); break;
+        case 1: return go(wtconv_norm_rows_bwd_kernel<T, 1, DROP>, smem);
+        case 2: return go(wtconv_norm_rows_bwd_kernel<T, 2, DROP>, smem);
+        case 3: return go(wtconv_norm_rows_bwd_kernel<T, 3, DROP>, smem);
+        case 4: return go(wtconv_norm_rows_bwd_kernel<T, 4, DROP>, smem);
         default:
-            if (a.dres || a.dx) wtconv_norm_rows_bwd_kernel<T, 0, DROP><<<grid, g.threads, 0, s>>>(m, a, d, g.tpr, vec);
+            if (a.dres || a.dx) go(wtconv_norm_rows_bwd_kernel<T, 0, DROP>, 0);
             return 0;  // no partial sums
     }
-    return (int)grid;
 }
 
 }  // namespace

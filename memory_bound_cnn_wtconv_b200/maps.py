@@ -114,6 +114,8 @@ def _desc(x: torch.Tensor, name: str) -> MapDesc:
         else:
             raise ValueError(f"{name} must be contiguous (NCHW) or channels-last contiguous (NHWC)")
         B, C, H, W = shape
+        if H == 0 or W == 0:
+            raise ValueError(f"{name} has no pixels: {tuple(shape)}")
     elif len(shape) == 2:
         if not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -122,8 +124,8 @@ def _desc(x: torch.Tensor, name: str) -> MapDesc:
         layout = NHWC
     else:
         raise ValueError(f"{name} must be a [B, C, H, W] map or [N, C] rows, got {len(shape)} dimensions")
-    if not (C > 0 and H > 0 and W > 0):
-        raise ValueError(f"{name} has no channels or no pixels: {tuple(shape)}")
+    if C == 0:
+        raise ValueError(f"{name} has no channels: {tuple(shape)}")
     return MapDesc(B, C, H, W, dtype, layout)
 
 
@@ -140,55 +142,58 @@ def _like(t: torch.Tensor, name: str, x: torch.Tensor, layout: int, dtype=None) 
 def _vector(t: torch.Tensor, name: str, x: torch.Tensor, shape) -> int:
     if t.dtype is not torch.float32 or t.device != x.device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor on {x.device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t.data_ptr()
 
 
 def _drop_ref(drop, x):
-    if drop is None:
-        return None
     if not isinstance(drop, Drop):
         raise TypeError(f"drop must be a Drop, got {type(drop).__name__}")
-    if isinstance(drop.offset, torch.Tensor) and drop.offset.device != x.device:
+    if drop._args.offset_dev is not None and drop.offset.device != x.device:
         raise ValueError(f"the offset tensor is on {drop.offset.device}, the activations on {x.device}")
     return ctypes.byref(drop._args)
 
 
 def _rows_shape(x: torch.Tensor):
-    return (x.shape[0],) if x.dim() == 2 else (x.shape[0], x.shape[2], x.shape[3])
+    s = x.shape
+    return s[:1] if len(s) == 2 else (s[0], s[2], s[3])
 
 
-def _on(x, stream, call):
-    """Run ``call`` with the stream, and the device of x, as the current ones."""
-    if stream is not None:
-        if stream.device != x.device:
-            raise ValueError(f"the stream is on {stream.device}, the activations on {x.device}")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    index = x.device.index
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            return call(torch.cuda.current_stream(index).cuda_stream)
-    return call(torch.cuda.current_stream(index).cuda_stream)
+def _elsewhere(x, stream) -> bool:
+    """Whether a call is not for the current stream of the current device."""
+    return stream is not None or x.get_device() != torch._C._cuda_getDevice()
+
+
+def _there(x, stream):
+    """The context in which that stream and the device of x are the current ones."""
+    if stream is None:
+        return torch.cuda.device(x.device)
+    if stream.device != x.device:
+        raise ValueError(f"the stream is on {stream.device}, the activations on {x.device}")
+    return torch.cuda.stream(stream)
+
+
+def _stream_of(x) -> int:
+    return torch._C._cuda_getCurrentRawStream(x.get_device())
 
 
 def dropout_forward(x, drop: Drop, residual=None, y=None, stream=None):
     """y = residual + drop(x) via ``wtconv_dropout``; returns y (allocated if
     not given)."""
-    lib = _lib()
     d = _desc(x, "x")
-    if drop is None:
-        raise TypeError("drop must be a Drop")
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return dropout_forward(x, drop, residual, y)
     ref = _drop_ref(drop, x)
-    rp = _like(residual, "residual", x, d.layout) if residual is not None else None
-
-    def call(s):
-        out = torch.empty_like(x) if y is None else y
-        _check(lib.wtconv_dropout(ctypes.byref(d), ref, x.data_ptr(), rp, _like(out, "y", x, d.layout), s),
-               "wtconv_dropout")
-        return out
-    return _on(x, stream, call)
+    rp = None if residual is None else _like(residual, "residual", x, d.layout)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _like(y, "y", x, d.layout)
+    _check(_lib().wtconv_dropout(ctypes.byref(d), ref, x.data_ptr(), rp, yp, _stream_of(x)), "wtconv_dropout")
+    return y
 
 
 def dropout_backward(dy, drop: Drop, dx=None, stream=None):
@@ -202,35 +207,47 @@ def rms_norm_forward(x, weight, residual=None, drop: Drop = None, eps: float = 1
     """h = residual + drop(x), y = h / rms(h) * weight via
     ``wtconv_rms_norm_forward``; returns (y, h, rstd).  Without a residual h is
     x itself.  ``rstd=False`` leaves rstd out (inference): None is returned."""
-    lib = _lib()
     d = _desc(x, "x")
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return rms_norm_forward(x, weight, residual, drop, eps, y, h, rstd)
     wp = _vector(weight, "weight", x, (d.C,))
-    ref = _drop_ref(drop, x)
-    rp = _like(residual, "residual", x, d.layout) if residual is not None else None
-    if residual is None and h is not None:
-        raise ValueError("without a residual, h is x: give none")
-
-    def call(s):
-        oy = torch.empty_like(x) if y is None else y
-        oh, hp = x, None
-        if residual is not None:
-            oh = torch.empty_like(x) if h is None else h
-            hp = _like(oh, "h", x, d.layout)
-        if rstd is False:
-            r, rsp = None, None
+    ref = None if drop is None else _drop_ref(drop, x)
+    if residual is None:
+        if h is not None:
+            raise ValueError("without a residual, h is x: give none")
+        h, rp, hp = x, None, None
+    else:
+        rp = _like(residual, "residual", x, d.layout)
+        if h is None:
+            h = torch.empty_like(x)
+            hp = h.data_ptr()
         else:
-            r = torch.empty(_rows_shape(x), dtype=torch.float32, device=x.device) if rstd is None else rstd
-            rsp = _vector(r, "rstd", x, _rows_shape(x))
-        _check(lib.wtconv_rms_norm_forward(ctypes.byref(d), eps, x.data_ptr(), rp, ref, wp,
-                                           _like(oy, "y", x, d.layout), hp, rsp, s), "wtconv_rms_norm_forward")
-        return oy, oh, r
-    return _on(x, stream, call)
+            hp = _like(h, "h", x, d.layout)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _like(y, "y", x, d.layout)
+    if rstd is None:
+        rstd = weight.new_empty(_rows_shape(x))
+        sp = rstd.data_ptr()
+    elif rstd is False:
+        rstd = sp = None
+    else:
+        sp = _vector(rstd, "rstd", x, _rows_shape(x))
+    _check(_lib().wtconv_rms_norm_forward(ctypes.byref(d), eps, x.data_ptr(), rp, ref, wp, yp, hp, sp, _stream_of(x)),
+           "wtconv_rms_norm_forward")
+    return y, h, rstd
 
 
 def rms_norm_workspace_bytes(x: torch.Tensor) -> int:
     """Workspace of ``rms_norm_backward`` for activations like x."""
     d = _desc(x, "x")
-    return _on(x, None, lambda s: int(_lib().wtconv_rms_norm_workspace_bytes(ctypes.byref(d))))
+    if _elsewhere(x, None):
+        with _there(x, None):
+            return rms_norm_workspace_bytes(x)
+    return _lib().wtconv_rms_norm_workspace_bytes(ctypes.byref(d))
 
 
 def rms_norm_backward(h, dy, weight, rstd, dh=None, drop: Drop = None, dx=None, dresidual=None, dweight=None,
@@ -238,51 +255,69 @@ def rms_norm_backward(h, dy, weight, rstd, dh=None, drop: Drop = None, dx=None, 
     """Gradients of ``rms_norm_forward`` from its h and rstd, via
     ``wtconv_rms_norm_backward``; ``dh`` is the gradient that reaches h itself.
     Returns (dx, dresidual, dweight).  Without ``drop`` (which has to be the
-    forward's) the two activations' gradients are the same tensor.
-    ``dresidual=False`` or ``dweight=False`` leaves that gradient out (None is
-    returned for it); ``dx=False`` too, with ``drop`` only.  ``workspace`` is a uint8 CUDA tensor of
-    at least ``rms_norm_workspace_bytes`` bytes; allocated here if not given."""
-    lib = _lib()
+    forward's) the two activations' gradients are the same tensor.  A gradient
+    given as False is left out (None is returned; without ``drop`` False for
+    either of the two stands for both).  ``workspace`` is a CUDA tensor of at
+    least ``rms_norm_workspace_bytes`` bytes; allocated here if not given."""
     d = _desc(h, "h")
-    dyp = _like(dy, "dy", h, d.layout)
+    if _elsewhere(h, stream):
+        with _there(h, stream):
+            return rms_norm_backward(h, dy, weight, rstd, dh, drop, dx, dresidual, dweight, workspace)
+    layout = d.layout
+    dyp = _like(dy, "dy", h, layout)
     wp = _vector(weight, "weight", h, (d.C,))
     rsp = _vector(rstd, "rstd", h, _rows_shape(h))
-    dhp = _like(dh, "dh", h, d.layout) if dh is not None else None
-    ref = _drop_ref(drop, h)
+    dhp = None if dh is None else _like(dh, "dh", h, layout)
+    gp = ref = None
     if drop is None:
-        if dx is not None and dx is not False and dresidual is not None and dresidual is not False and dx is not dresidual:
-            raise ValueError("without dropout dx and dresidual are the same: give one")
-        skip = dx is False or dresidual is False
-        same = (dx if dx is not None else dresidual) if not skip else False
-
-    def call(s):
-        if drop is None:
-            r = None if same is False else torch.empty_like(h) if same is None else same
-            g, gp = r, None
+        if dx is False or dresidual is False:
+            dresidual = False
+        elif dx is not None:
+            if dresidual is not None and dresidual is not dx:
+                raise ValueError("without dropout dx and dresidual are the same: give one")
+            dresidual = dx
+    else:
+        ref = _drop_ref(drop, h)
+        if dx is None:
+            dx = torch.empty_like(h)
+            gp = dx.data_ptr()
+        elif dx is False:
+            dx = None
         else:
-            r = None if dresidual is False else torch.empty_like(h) if dresidual is None else dresidual
-            g = None if dx is False else torch.empty_like(h) if dx is None else dx
-            gp = None if g is None else _like(g, "dx", h, d.layout)
-        rp = None if r is None else _like(r, "dresidual", h, d.layout)
-        w = ws = wwp = wsp = None
-        nbytes = 0
-        if dweight is not False:
-            w = torch.empty((d.C,), dtype=torch.float32, device=h.device) if dweight is None else dweight
-            wwp = _vector(w, "dweight", h, (d.C,))
-            if workspace is None:
-                nbytes = lib.wtconv_rms_norm_workspace_bytes(ctypes.byref(d))
-                if nbytes:
-                    ws = torch.empty((nbytes,), dtype=torch.uint8, device=h.device)
-                    wsp = ws.data_ptr()
-            else:
-                if not workspace.is_cuda or workspace.device != h.device or not workspace.is_contiguous():
-                    raise ValueError(f"workspace must be a contiguous tensor on {h.device}")
-                wsp, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        if rp is not None or gp is not None or wwp is not None:
-            _check(lib.wtconv_rms_norm_backward(ctypes.byref(d), h.data_ptr(), dyp, dhp, ref, wp, rsp, rp, gp, wwp,
-                                                wsp, nbytes, s), "wtconv_rms_norm_backward")
-        return g, r, w
-    return _on(h, stream, call)
+            gp = _like(dx, "dx", h, layout)
+    if dresidual is None:
+        dresidual = torch.empty_like(h)
+        rp = dresidual.data_ptr()
+    elif dresidual is False:
+        dresidual = rp = None
+    else:
+        rp = _like(dresidual, "dresidual", h, layout)
+    if drop is None:
+        dx = dresidual
+    lib = _lib()
+    wsp = None
+    nbytes = 0
+    if dweight is False:
+        dweight = dwp = None
+        if rp is None and gp is None:
+            return dx, dresidual, None
+    else:
+        if dweight is None:
+            dweight = torch.empty_like(weight)
+            dwp = dweight.data_ptr()
+        else:
+            dwp = _vector(dweight, "dweight", h, (d.C,))
+        if workspace is None:
+            nbytes = lib.wtconv_rms_norm_workspace_bytes(ctypes.byref(d))
+            workspace = weight.new_empty(((nbytes + 3) // 4,))
+            wsp = workspace.data_ptr()
+        else:
+            if not workspace.is_cuda or workspace.device != h.device or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on {h.device}")
+            wsp, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.wtconv_rms_norm_backward(ctypes.byref(d), h.data_ptr(), dyp, dhp, ref, wp, rsp, rp, gp, dwp, wsp, nbytes,
+                                        _stream_of(h)), "wtconv_rms_norm_backward")
+    return dx, dresidual, dweight
 
 
 def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, dtype=torch.float8_e4m3fn, group: int = 0, q=None,
@@ -292,35 +327,45 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, dtype=torch.float8_
     of a pixel (32, 64, 128, or 0: all), via ``wtconv_rms_norm_q8``; q * scale
     stands for the norm.  Returns (q, scale, h): scale is [B, groups, H, W] (or
     [N, groups]) in the layout of x; h is x without a residual."""
-    lib = _lib()
     if dtype not in _Q8:
         raise TypeError(f"dtype must be torch.float8_e4m3fn or torch.int8, got {dtype}")
     if group not in (0, 32, 64, 128):
         raise ValueError(f"group must be 0, 32, 64 or 128, got {group}")
     d = _desc(x, "x")
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return rms_norm_q8(x, weight, residual, eps, dtype, group, q, scale, h)
+    layout = d.layout
     wp = _vector(weight, "weight", x, (d.C,))
-    rp = _like(residual, "residual", x, d.layout) if residual is not None else None
-    if residual is None and h is not None:
-        raise ValueError("without a residual, h is x: give none")
+    if residual is None:
+        if h is not None:
+            raise ValueError("without a residual, h is x: give none")
+        h, rp, hp = x, None, None
+    else:
+        rp = _like(residual, "residual", x, layout)
+        if h is None:
+            h = torch.empty_like(x)
+            hp = h.data_ptr()
+        else:
+            hp = _like(h, "h", x, layout)
+    if q is None:
+        q = torch.empty_like(x, dtype=dtype)
+        qp = q.data_ptr()
+    else:
+        qp = _like(q, "q", x, layout, dtype)
     groups = -(-d.C // group) if group else 1
-    sshape = (x.shape[0], groups, *x.shape[2:])
-    fmt = torch.channels_last if d.layout == NHWC and x.dim() == 4 else torch.contiguous_format
-
-    def call(s):
-        oq = torch.empty_like(x, dtype=dtype) if q is None else q
-        qp = _like(oq, "q", x, d.layout, dtype)
-        sc = torch.empty(sshape, dtype=torch.float32, device=x.device, memory_format=fmt) if scale is None else scale
-        if sc.dtype is not torch.float32 or tuple(sc.shape) != sshape or sc.device != x.device \
-                or not sc.is_contiguous(memory_format=fmt):
-            raise ValueError(f"scale must be a float32 tensor of shape {sshape} in the layout of x on {x.device}")
-        oh, hp = x, None
-        if residual is not None:
-            oh = torch.empty_like(x) if h is None else h
-            hp = _like(oh, "h", x, d.layout)
-        _check(lib.wtconv_rms_norm_q8(ctypes.byref(d), eps, x.data_ptr(), rp, wp, _Q8[dtype], group, qp,
-                                      sc.data_ptr(), hp, s), "wtconv_rms_norm_q8")
-        return oq, sc, oh
-    return _on(x, stream, call)
+    shape = (x.shape[0], groups, *x.shape[2:])
+    nhwc = layout == NHWC and x.dim() == 4
+    if scale is None:
+        scale = weight.new_empty((shape[0], *shape[2:], groups) if nhwc else shape)
+        if nhwc:
+            scale = scale.permute(0, 3, 1, 2)
+    elif scale.dtype is not torch.float32 or scale.shape != shape or scale.device != x.device \
+            or not scale.is_contiguous(memory_format=torch.channels_last if nhwc else torch.contiguous_format):
+        raise ValueError(f"scale must be a float32 tensor of shape {shape} in the layout of x on {x.device}")
+    _check(_lib().wtconv_rms_norm_q8(ctypes.byref(d), eps, x.data_ptr(), rp, wp, _Q8[dtype], group, qp,
+                                     scale.data_ptr(), hp, _stream_of(x)), "wtconv_rms_norm_q8")
+    return q, scale, h
 
 
 def _laid_out(x):
