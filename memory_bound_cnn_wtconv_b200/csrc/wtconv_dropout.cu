@@ -129,16 +129,19 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_spans_kernel(MapShape
         const uint4* xv = reinterpret_cast<const uint4*>(x + head);
         const uint4* rv = reinterpret_cast<const uint4*>(res + head);
         uint4* yv = reinterpret_cast<uint4*>(y + head);
+        if (keep) {
 #pragma unroll 4
-        for (long long i = first; i < body; i += step) {
-            float f[V] = {}, r[V] = {};
-            if (RES) unpack(rv[i], r);
-            if (keep) unpack(xv[i], f);
-            if (keep) {
+            for (long long i = first; i < body; i += step) {
+                float f[V], r[V] = {};
+                unpack(xv[i], f);
+                if (RES) unpack(rv[i], r);
 #pragma unroll
                 for (int e = 0; e < V; ++e) r[e] = __fmaf_rn(f[e], d.grown, r[e]);
+                yv[i] = pack(r);
             }
-            yv[i] = pack(r);
+        } else {
+#pragma unroll 4
+            for (long long i = first; i < body; i += step) yv[i] = RES ? rv[i] : make_uint4(0, 0, 0, 0);
         }
         for (long long i = first; i < head; i += step) one(i);
         for (long long i = head + body * V + first; i < len; i += step) one(i);

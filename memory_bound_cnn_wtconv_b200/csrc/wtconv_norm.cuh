@@ -15,6 +15,13 @@ constexpr int kNormParts = 8;
 
 inline long long norm_parts(const MapShape& m, int sms) { return std::min(m.rows, (long long)kNormParts * sms); }
 
+// CTAs of a kernel that an SM holds.
+template <typename K>
+int norm_resident(K kernel, int threads, size_t smem) {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) == cudaSuccess && n > 0 ? n : 1;
+}
+
 // How JOIN reads h: x itself, residual + x, or residual + dropout of x.
 enum { kPlain = 0, kResidual = 1, kDropped = 2 };
 

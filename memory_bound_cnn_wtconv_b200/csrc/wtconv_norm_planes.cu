@@ -1,478 +1,447 @@
 // RMS norm of maps whose pixels are adjacent (NCHW).
 //
-// A CTA holds a tile of LP * VP neighbouring pixels of one sample with all
-// their channels.  LP lanes of a warp lie along the pixels, VP of them each (a
-// 16-byte chunk, or one value where planes are not whole chunks); the other
+// A CTA walks tiles of lp * VP neighbouring pixels of one sample with all their
+// channels.  lp lanes of a warp lie along the pixels, VP of them each; the other
 // lanes and the warps share out the channels in quads of four, since a random
-// word quad covers four channels: owner o has the quads o, o + owners, ..., G
-// of them, in registers between the sum of squares and the output.  G = 0 is
-// for more channels than a CTA's registers hold: they are read again.
+// word quad covers four channels: owner o has the quads o, o + owners, ...
 //
-// Bound by memory, like the kernels of adjacent channels.  The squares are
-// summed over an owner's channels, the lanes, then the warps (through shared
-// memory: one sum a pixel and warp).  The backward's CTAs walk the tiles with
-// the weight gradient's sums of their own channels in registers.
-#include "wtconv_norm.cuh"
+// The inputs of the next tile come into shared memory (cp.async, 16 bytes)
+// while this one is computed.  VP = 16 bytes of pixels where planes are whole
+// 16-byte chunks: each thread copies the chunks that it owns itself, so nothing
+// but its own copies has to arrive.  VP = 1 where they are not: each channel's
+// pixels come as the aligned chunks that cover them, shifted by the plane's own
+// distance from a 16-byte boundary, and are read value by value.
+//
+// Bound by memory.  Without the copies ahead a CTA loads, waits, sums and
+// stores in turn, and too few CTAs fit an SM to hide it: 388 us for the
+// backward of 32 x 512 x 64 x 64 fp32 with the gradient of h.
+//
+// The squares are summed over an owner's channels, the lanes, then the warps
+// (tile_sum).  The weight gradient's sums of a thread's own channels stay in
+// its registers for all its tiles.
+#include "wtconv_norm_planes.cuh"
 
 namespace wtc {
 
 namespace {
 
+constexpr int kMaxWarps = 16;
+constexpr int kSmem = 200 * 1024;      // of the 227 KB a CTA may have
+constexpr int kSmemTwo = 110 * 1024;   // two CTAs an SM
+
 struct PlanesGeom {
-    int lp, g, warps;
-    int tiles;  // of a plane
-    int owners;
+    int lp, warps, owners, iters;  // iters: quads of an owner
+    int tiles;                     // of a plane
+    int row;                       // VP = 1: bytes of a channel's pixels in a stage
+    int tensor;                    // bytes of one tensor in a stage
+    int head;                      // bytes of both stages
+    FastDiv by_chunks;             // VP = 1: row / 16
 };
 
-constexpr int kMaxWarps = 16;
-
-// Pixel lanes: 8 (with 16-byte chunks 128 adjacent bytes) unless the channels
-// are few (more pixels, so that no owner is idle) or many (fewer, so that a
-// CTA's registers hold them); single values want more lanes for the same bytes.
-PlanesGeom planes_geom(const MapShape& m, int VP, const int* gs, int ngs) {
+// Tiles of 128 bytes of a plane (all 32 lanes' single values where planes are
+// not whole chunks), less where two stages of `tensors` tensors do not leave
+// room for two CTAs on an SM, down to 64 bytes, and then what fits at all.
+// False if nothing does.
+bool planes_geom(const MapShape& m, int VP, int esize, int tensors, int most_iters, PlanesGeom* out) {
     const int quads = (m.C + 3) / 4;
-    PlanesGeom g{};
     int lp = VP == 1 ? 32 : 8;
     while (lp < 32 && quads * lp <= 16) lp *= 2;
     while (lp > 1 && lp / 2 * VP >= m.HW) lp /= 2;
-    for (;; lp /= 2) {
+    for (; lp >= 1; lp /= 2) {
+        PlanesGeom g{};
         const int lanes = 32 / lp;
-        for (int i = 0; i < ngs; ++i) {
-            const int warps = (quads + lanes * gs[i] - 1) / (lanes * gs[i]);
-            if (warps <= (i + 1 < ngs ? kMaxWarps / 2 : kMaxWarps)) {
-                g.lp = lp, g.g = gs[i], g.warps = warps;
-                break;
-            }
-        }
-        if (g.lp || lp == 1) break;
+        g.lp = lp;
+        g.iters = 1;
+        while (g.iters < most_iters && (quads + lanes * g.iters - 1) / (lanes * g.iters) > 8) g.iters *= 2;
+        g.warps = (quads + lanes * g.iters - 1) / (lanes * g.iters);
+        if (g.warps > kMaxWarps) continue;
+        g.owners = g.warps * lanes;
+        g.tiles = (m.HW + lp * VP - 1) / (lp * VP);
+        g.row = (lp * esize + 15) / 16 * 16 + 16;
+        const long long tensor = VP == 1 ? (long long)g.row * m.C : 64LL * g.iters * g.warps * 32;
+        if (2 * tensors * tensor > kSmem) continue;
+        if (2 * tensors * tensor > kSmemTwo && lp > (VP == 1 ? 16 : 4)) continue;
+        g.tensor = (int)tensor;
+        g.head = (int)(2 * tensors * tensor);
+        g.by_chunks = make_fastdiv(g.row / 16);
+        *out = g;
+        return true;
     }
-    if (!g.lp) g.lp = 8, g.g = 0, g.warps = kMaxWarps;
-    g.owners = g.warps * (32 / g.lp);
-    g.tiles = (m.HW + g.lp * VP - 1) / (g.lp * VP);
-    return g;
+    return false;
 }
+
+__device__ __forceinline__ void copy16(void* to, const void* from, int bytes) {  // the rest of the 16 bytes as zeros
+    const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(to));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
 template <typename T, int VP>
-using Raw = typename Chunk<T, VP>::type;
+struct Tile {
+    using R = typename Chunk<T, VP>::type;
 
-// 4 * VP keep bits: bit j * VP + v is channel 4 * quad + j of pixel v.
-template <int VP>
-__device__ __forceinline__ uint32_t keep_tile(const MapDrop& d, uint32_t offset, long long row, long long b, int quad) {
-    uint32_t bits = 0;
-    if (d.mode == WTCONV_DROP_ELEMENT) {
-#pragma unroll
-        for (int v = 0; v < VP; ++v) {
-            const uint32_t k = keep_bits(d, drop_words(d, offset, row + v, quad));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) bits |= (k >> j & 1) << (j * VP + v);
+    const MapShape& m;
+    const PlanesGeom& geom;
+    char* smem;
+    int pl, owner;
+    long long b;
+    int p0, p;       // first pixel of the tile, of this thread
+    bool live;
+
+    __device__ __forceinline__ Tile(const MapShape& shape, const PlanesGeom& g, char* s) : m(shape), geom(g), smem(s) {
+        const int lane = threadIdx.x % 32;
+        pl = lane & (geom.lp - 1);
+        owner = (threadIdx.x / 32) * (32 / geom.lp) + lane / geom.lp;
+    }
+    __device__ __forceinline__ void at(long long tile) {
+        b = tile / geom.tiles;
+        p0 = (int)(tile - b * geom.tiles) * geom.lp * VP;
+        p = p0 + pl * VP;
+        live = p < m.HW;  // with chunks, HW is a multiple of VP
+    }
+    __device__ __forceinline__ int quad(int g) const { return g * geom.owners + owner; }
+    __device__ __forceinline__ bool in(int c) const { return live && c < m.C; }
+    // Element (channel c, this thread's pixel) of the map.
+    __device__ __forceinline__ long long element(int c) const { return (b * m.C + c) * m.HW + p; }
+
+    // This thread's chunk of channel 4 * quad(g) + j of tensor k, in shared memory.
+    __device__ __forceinline__ R* slot(int stage, int tensors, int k, int g, int j) const {
+        char* s = smem + (stage * tensors + k) * geom.tensor;
+        if constexpr (VP == 1) {
+            const int c = 4 * quad(g) + j;
+            const uint32_t first = (uint32_t)((b * m.C + c) * m.HW + p0) * (uint32_t)sizeof(T);  // modulo 2^32
+            return reinterpret_cast<R*>(s + c * geom.row + (first & 15) + pl * sizeof(T));
+        } else {
+            return reinterpret_cast<R*>(s) + (4 * g + j) * blockDim.x + threadIdx.x;
         }
-    } else {
-        const uint32_t k = keep_bits(d, drop_words(d, offset, b, quad));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) bits |= k >> j & 1 ? ((1u << VP) - 1) << (j * VP) : 0u;
     }
-    return bits;
-}
+    // Starts the copy of tensor k of this tile; with skip, zeros.
+    __device__ __forceinline__ void fetch(int stage, int tensors, int k, const void* from, bool skip) const {
+        if constexpr (VP == 1) {
+            const long long bytes = m.rows * m.C * (long long)sizeof(T);
+            const int pixels = min(geom.lp, m.HW - p0), chunks = geom.row / 16;
+            char* s = smem + (stage * tensors + k) * geom.tensor;
+            const int n = m.C * chunks;
+            for (int i = threadIdx.x; i < n; i += blockDim.x) {
+                const int c = (int)((__umulhi((uint32_t)i, geom.by_chunks.mul) + (uint32_t)i) >> geom.by_chunks.shift);
+                const int q = i - c * chunks;
+                const long long first = ((b * m.C + c) * m.HW + p0) * (long long)sizeof(T);
+                const int span = (int)(first & 15) + pixels * (int)sizeof(T);  // from the chunk boundary on
+                if (16 * q >= span) continue;
+                const long long at = (first & ~15LL) + 16 * q;
+                copy16(s + c * geom.row + 16 * q, static_cast<const char*>(from) + at, skip ? 0 : (int)min(16LL, bytes - at));
+            }
+        } else {
+            for (int g = 0; g < geom.iters; ++g) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = 4 * quad(g) + j;
+                    const bool ok = in(c) && !skip;
+                    copy16(slot(stage, tensors, k, g, j), static_cast<const T*>(from) + (ok ? element(c) : 0), ok ? 16 : 0);
+                }
+            }
+        }
+    }
+    // The oldest of two stages has arrived (and, where threads read what others
+    // copied, for all of them; their reads of the other stage are over).
+    __device__ __forceinline__ void arrive() const {
+        copies_wait<0>();
+        if constexpr (VP == 1) __syncthreads();
+    }
+};
 
-// One sum for each pixel of the tile over all owners, or a function of it:
-// `finish(pixel of the tile, sum)` runs once a pixel, its results are handed to
-// every owner.  smem: [warps + 1][LP * VP] floats.
-template <int VP, typename F>
-__device__ __forceinline__ void tile_sum(float (&v)[VP], int lp, float* smem, F finish) {
-    const int warps = blockDim.x / 32, lane = threadIdx.x % 32, pl = lane & (lp - 1), px = lp * VP;
-    for (int o = lp; o < 32; o *= 2) {
-#pragma unroll
-        for (int e = 0; e < VP; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
-    }
-    if (lane < lp) {
-#pragma unroll
-        for (int e = 0; e < VP; ++e) smem[(threadIdx.x / 32) * px + pl * VP + e] = v[e];
-    }
-    __syncthreads();
-    for (int p = threadIdx.x; p < px; p += blockDim.x) {
-        float s = smem[p];
-        for (int k = 1; k < warps; ++k) s += smem[k * px + p];
-        smem[warps * px + p] = finish(p, s);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < VP; ++e) v[e] = smem[warps * px + pl * VP + e];
-}
-
-template <typename T, int VP, int G, int JOIN, bool Q8>
+template <typename T, int VP, int JOIN, bool Q8>
 __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapShape m, NormFwdArgs a, MapDrop d, PlanesGeom geom) {
-    constexpr int GR = G ? G : 1;
-    using R = Raw<T, VP>;
-    using C4 = Chunk<T, VP>;
-    extern __shared__ float smem[];  // tile_sum's, then (Q8) the groups' largest bits: [groups][LP * VP]
-    const int lp = geom.lp, px = lp * VP, warps = blockDim.x / 32, lane = threadIdx.x % 32;
-    const int pl = lane & (lp - 1), owner = (threadIdx.x / 32) * (32 / lp) + lane / lp;
-    const int iters = G ? G : (m.C + 4 * geom.owners - 1) / (4 * geom.owners);
+    using R = typename Chunk<T, VP>::type;
+    constexpr int NT = JOIN == kPlain ? 1 : 2;
+    extern __shared__ __align__(16) char smem[];  // two stages; tile_sum's; (Q8) the groups' largest bits: [groups][px]
+    float* sums = reinterpret_cast<float*>(smem + geom.head);
+    const int px = geom.lp * VP, warps = blockDim.x / 32;
     const uint32_t offset = JOIN == kDropped ? drop_offset(d) : 0;
     const long long total = m.rows / m.HW * geom.tiles;
-    for (long long tile = blockIdx.x; tile < total; tile += gridDim.x) {
-        const long long b = tile / geom.tiles;
-        const int p0 = (int)(tile - b * geom.tiles) * px, p = p0 + pl * VP;
-        const bool live = p < m.HW;  // with chunks, HW is a multiple of VP
-        const long long base = b * m.C * m.HW + p, row = b * m.HW + p;
-        const T* x = static_cast<const T*>(a.x) + base;
-        const T* res = static_cast<const T*>(a.residual) + base;
-        T* h = static_cast<T*>(a.h) + base;
+    Tile<T, VP> now(m, geom, smem), next(m, geom, smem);
+    auto fetch = [&](const Tile<T, VP>& t, int stage) {
+        bool skip = false;
+        if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) skip = !keep_sample(d, offset, t.b);
+        t.fetch(stage, NT, 0, a.x, skip);
+        if (JOIN != kPlain) t.fetch(stage, NT, 1, a.residual, false);
+        copies_commit();
+    };
+    next.at(blockIdx.x);
+    fetch(next, 0);
+    int stage = 0;
+    for (long long tile = blockIdx.x; tile < total; tile += gridDim.x, stage ^= 1) {
+        now.at(tile);
+        now.arrive();
+        if (tile + gridDim.x < total) next.at(tile + gridDim.x), fetch(next, stage ^ 1);
+        const long long row = now.b * m.HW + now.p;
         bool whole = true;
-        if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, b);
-        R raw[GR][4], rr[GR][4];
+        if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, now.b);
         float ss[VP] = {};
-        auto load = [&](int g, R (&rx)[4], R (&rres)[4]) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = 4 * (g * geom.owners + owner) + j;
-                const bool in = live && c < m.C;
-                const long long at = (long long)c * m.HW;
-                rx[j] = in && whole ? *reinterpret_cast<const R*>(x + at) : C4::zero();
-                if (JOIN != kPlain) rres[j] = in ? *reinterpret_cast<const R*>(res + at) : C4::zero();
-            }
-        };
-        auto join = [&](int g, R (&rx)[4], const R (&rres)[4]) {
-            const int quad = g * geom.owners + owner;
+        for (int g = 0; g < geom.iters; ++g) {
+            const int quad = now.quad(g);
             uint32_t keep = whole ? 0xffffffffu : 0u;
             if (JOIN == kDropped && d.mode != WTCONV_DROP_SAMPLE && 4 * quad < m.C)
-                keep = keep_tile<VP>(d, offset, row, b, quad);
+                keep = keep_tile<VP>(d, offset, row, now.b, quad);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                if (!now.in(4 * quad + j)) continue;
+                R* at = now.slot(stage, NT, 0, g, j);
                 float f[VP];
-                unpack(rx[j], f);
+                unpack(*at, f);
                 if (JOIN != kPlain) {
                     float r[VP];
-                    unpack(rres[j], r);
+                    unpack(*now.slot(stage, NT, 1, g, j), r);
 #pragma unroll
                     for (int e = 0; e < VP; ++e) {
-                        if (JOIN == kDropped) f[e] = keep >> (j * VP + e) & 1 ? __fmaf_rn(f[e], d.grown, r[e]) : r[e];
-                        else f[e] += r[e];
+                        if (JOIN != kDropped) r[e] += f[e];
+                        else if (keep >> (j * VP + e) & 1) r[e] = __fmaf_rn(f[e], d.grown, r[e]);
                     }
-                    rx[j] = C4::from(f);
-                    if (live && 4 * quad + j < m.C) *reinterpret_cast<R*>(h + (long long)(4 * quad + j) * m.HW) = rx[j];
-                    unpack(rx[j], f);  // the norm is of h as it is stored
+                    const R h = Chunk<T, VP>::from(r);
+                    *reinterpret_cast<R*>(static_cast<T*>(a.h) + now.element(4 * quad + j)) = h;
+                    *at = h;
+                    unpack(h, f);  // the norm is of h as it is stored
                 }
 #pragma unroll
                 for (int e = 0; e < VP; ++e) ss[e] += f[e] * f[e];
             }
-        };
-        if (G) {
-#pragma unroll
-            for (int g = 0; g < GR; ++g) load(g, raw[g], rr[g]);
-#pragma unroll
-            for (int g = 0; g < GR; ++g) join(g, raw[g], rr[g]);
-        } else {
-            for (int g = 0; g < iters; ++g) load(g, raw[0], rr[0]), join(g, raw[0], rr[0]);
         }
-        tile_sum<VP>(ss, lp, smem, [&](int q, float s) {
+        tile_sum<VP>(ss, geom.lp, sums, [&](int q, float s) {
             const float r = rsqrtf(s / m.C + a.eps);
-            if (a.rstd && p0 + q < m.HW) a.rstd[b * m.HW + p0 + q] = r;
+            if (a.rstd && now.p0 + q < m.HW) a.rstd[now.b * m.HW + now.p0 + q] = r;
             return r;
         });
-        // v = h * r * w of channel j of round g; false where there is none
-        auto value = [&](int g, int j, R hraw, float (&f)[VP]) {
-            const int c = 4 * (g * geom.owners + owner) + j;
-            if (!live || c >= m.C) return false;
-            if (!G) hraw = *reinterpret_cast<const R*>((JOIN == kPlain ? x : h) + (long long)c * m.HW);  // this thread's own
+        // v = h * r * w of channel c
+        auto value = [&](int g, int j, int c, float (&f)[VP]) {
             const float w = a.weight[c];
-            unpack(hraw, f);
+            unpack(*now.slot(stage, NT, 0, g, j), f);
 #pragma unroll
             for (int e = 0; e < VP; ++e) f[e] = f[e] * ss[e] * w;
-            return true;
         };
         if (!Q8) {
-            auto out = [&](int g, const R (&hraw)[4]) {
+            for (int g = 0; g < geom.iters; ++g) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    const int c = 4 * now.quad(g) + j;
+                    if (!now.in(c)) continue;
                     float f[VP];
-                    if (value(g, j, hraw[j], f))
-                        *reinterpret_cast<R*>(static_cast<T*>(a.y) + base + (long long)(4 * (g * geom.owners + owner) + j) * m.HW) = C4::from(f);
+                    value(g, j, c, f);
+                    *reinterpret_cast<R*>(static_cast<T*>(a.y) + now.element(c)) = Chunk<T, VP>::from(f);
                 }
-            };
-            if (G) {
-#pragma unroll
-                for (int g = 0; g < GR; ++g) out(g, raw[g]);
-            } else {
-                for (int g = 0; g < iters; ++g) out(g, raw[0]);
             }
         } else {
-            uint32_t* top = reinterpret_cast<uint32_t*>(smem + (warps + 1) * px);
+            uint32_t* top = reinterpret_cast<uint32_t*>(sums + (warps + 1) * px);
             const int groups = (m.C + a.group - 1) / a.group;
-            // Largest |v| of the quad's group among this thread's channels, for each of its pixels.
-            auto largest = [&](int g, const R (&hraw)[4], uint32_t (&bits)[VP]) {
+            for (int q = threadIdx.x; q < groups * px; q += blockDim.x) top[q] = 0;
+            __syncthreads();
+            for (int g = 0; g < geom.iters; ++g) {
+                const int c0 = 4 * now.quad(g);
+                uint32_t bits[VP] = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    if (!now.in(c0 + j)) continue;
                     float f[VP];
-                    if (value(g, j, hraw[j], f)) {
+                    value(g, j, c0 + j, f);
 #pragma unroll
-                        for (int e = 0; e < VP; ++e) bits[e] = max(bits[e], abs_bits(f[e]));
-                    }
+                    for (int e = 0; e < VP; ++e) bits[e] = max(bits[e], abs_bits(f[e]));
                 }
-            };
-            // The groups of channels c0 .. c0 + n * group - 1 in `top`, then their scales in its place.
-            auto clear = [&](int n) {
-                for (int q = threadIdx.x; q < n * px; q += blockDim.x) top[q] = 0;
-                __syncthreads();
-            };
-            auto give = [&](int first, int n) {
-                __syncthreads();
-                for (int q = threadIdx.x; q < n * px; q += blockDim.x) {
-                    const float s = q8_scale(top[q], a.q8);
-                    top[q] = __float_as_uint(s);
-                    const int gr = first + q / px, pp = p0 + q % px;
-                    if (gr < groups && pp < m.HW) a.scale[(b * groups + gr) * m.HW + pp] = s;
-                }
-                __syncthreads();
-            };
-            auto note = [&](int at, const uint32_t (&bits)[VP]) {
-                if (!live) return;
+                if (now.in(c0)) {
 #pragma unroll
-                for (int e = 0; e < VP; ++e) atomicMax(&top[at * px + pl * VP + e], bits[e]);
-            };
-            auto out = [&](int g, int first, const R (&hraw)[4]) {
-                uint8_t* q = static_cast<uint8_t*>(a.y) + base;
-                const int c0 = 4 * (g * geom.owners + owner);
-                const int at = c0 / a.group - first;
-                float s[VP];
-                if (c0 < m.C) {
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) s[e] = 1.0f / __uint_as_float(top[at * px + pl * VP + e]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float f[VP];
-                    if (!value(g, j, hraw[j], f)) continue;
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) f[e] *= s[e];  // one rounding more than v / scale
-                    uint8_t* o = q + (long long)(c0 + j) * m.HW;
-                    if constexpr (VP == 1) {
-                        *o = (uint8_t)q8_pack4(f[0], 0.0f, 0.0f, 0.0f, a.q8);
-                    } else if constexpr (VP == 4) {
-                        *reinterpret_cast<uint32_t*>(o) = q8_pack4(f[0], f[1], f[2], f[3], a.q8);
-                    } else {
-                        *reinterpret_cast<uint2*>(o) = make_uint2(q8_pack4(f[0], f[1], f[2], f[3], a.q8),
-                                                                  q8_pack4(f[4], f[5], f[6], f[7], a.q8));
-                    }
-                }
-            };
-            // All groups at once where the registers hold the row, or the row is one group; else round by round (a
-            // round is 4 * owners channels, a multiple of 128: whole groups).
-            if (G || groups == 1) {
-                clear(groups);
-                if (G) {
-#pragma unroll
-                    for (int g = 0; g < GR; ++g) {
-                        const int c0 = 4 * (g * geom.owners + owner);
-                        uint32_t bits[VP] = {};
-                        largest(g, raw[g], bits);
-                        if (c0 < m.C) note(c0 / a.group, bits);
-                    }
-                } else {
-                    uint32_t bits[VP] = {};
-                    for (int g = 0; g < iters; ++g) largest(g, raw[0], bits);
-                    note(0, bits);
-                }
-                give(0, groups);
-                if (G) {
-#pragma unroll
-                    for (int g = 0; g < GR; ++g) out(g, 0, raw[g]);
-                } else {
-                    for (int g = 0; g < iters; ++g) out(g, 0, raw[0]);
-                }
-                __syncthreads();  // before the next tile's clear
-            } else {
-                const int n = 4 * geom.owners / a.group;
-                for (int g = 0; g < iters; ++g) {
-                    clear(n);
-                    uint32_t bits[VP] = {};
-                    const int c0 = 4 * (g * geom.owners + owner);
-                    largest(g, raw[0], bits);
-                    if (c0 < m.C) note(c0 / a.group - g * n, bits);
-                    give(g * n, n);
-                    out(g, g * n, raw[0]);
-                    __syncthreads();
+                    for (int e = 0; e < VP; ++e) atomicMax(&top[c0 / a.group * px + now.pl * VP + e], bits[e]);
                 }
             }
+            __syncthreads();
+            for (int q = threadIdx.x; q < groups * px; q += blockDim.x) {
+                const float s = q8_scale(top[q], a.q8);
+                top[q] = __float_as_uint(1.0f / s);  // one rounding more than v / scale
+                const int pixel = now.p0 + q % px;
+                if (pixel < m.HW) a.scale[(now.b * groups + q / px) * m.HW + pixel] = s;
+            }
+            __syncthreads();
+            for (int g = 0; g < geom.iters; ++g) {
+                const int c0 = 4 * now.quad(g);
+                float inv[VP];
+                if (c0 < m.C) {
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) inv[e] = __uint_as_float(top[c0 / a.group * px + now.pl * VP + e]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!now.in(c0 + j)) continue;
+                    float f[VP];
+                    value(g, j, c0 + j, f);
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) f[e] *= inv[e];
+                    q8_store<VP>(static_cast<uint8_t*>(a.y) + now.element(c0 + j), f, a.q8);
+                }
+            }
+            __syncthreads();  // before the next tile clears `top`
         }
     }
 }
 
+// G: quads of an owner (geom.iters), at compile time for the sums in registers.
 template <typename T, int VP, int G, bool DROP>
 __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(MapShape m, NormBwdArgs a, MapDrop d, PlanesGeom geom) {
-    constexpr int GR = G ? G : 1;
-    using R = Raw<T, VP>;
-    using C4 = Chunk<T, VP>;
-    extern __shared__ float smem[];
-    const int lp = geom.lp, px = lp * VP, lane = threadIdx.x % 32;
-    const int pl = lane & (lp - 1), owner = (threadIdx.x / 32) * (32 / lp) + lane / lp;
-    const int iters = G ? G : (m.C + 4 * geom.owners - 1) / (4 * geom.owners);
+    using R = typename Chunk<T, VP>::type;
+    extern __shared__ __align__(16) char smem[];
+    float* sums = reinterpret_cast<float*>(smem + geom.head);
+    const int NT = a.dh ? 3 : 2;
     const uint32_t offset = DROP ? drop_offset(d) : 0;
     const long long total = m.rows / m.HW * geom.tiles;
-    float acc[GR][4] = {};
-    for (long long tile = blockIdx.x; tile < total; tile += gridDim.x) {
-        const long long b = tile / geom.tiles;
-        const int p = (int)(tile - b * geom.tiles) * px + pl * VP;
-        const bool live = p < m.HW;
-        const long long base = b * m.C * m.HW + p, row = b * m.HW + p;
-        const T* h = static_cast<const T*>(a.h) + base;
-        const T* dy = static_cast<const T*>(a.dy) + base;
-        const T* dh = static_cast<const T*>(a.dh) + base;
-        bool whole = true;
-        if (DROP && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, b);
-        float r[VP] = {};
-        if (live) {
+    const bool outputs = a.dres || (DROP && a.dx);
+    Tile<T, VP> now(m, geom, smem), next(m, geom, smem);
+    auto fetch = [&](const Tile<T, VP>& t, int stage) {
+        t.fetch(stage, NT, 0, a.h, false);
+        t.fetch(stage, NT, 1, a.dy, false);
+        if (a.dh) t.fetch(stage, NT, 2, a.dh, false);
+        copies_commit();
+    };
+    float acc[G][4] = {};
+    next.at(blockIdx.x);
+    fetch(next, 0);
+    int stage = 0;
+    for (long long tile = blockIdx.x; tile < total; tile += gridDim.x, stage ^= 1) {
+        now.at(tile);
+        float r[VP] = {}, gh[VP] = {};
+        const long long row = now.b * m.HW + now.p;
+        if (now.live) {
 #pragma unroll
             for (int e = 0; e < VP; ++e) r[e] = a.rstd[row + e];
         }
-        R hr[GR][4], gr[GR][4];
-        float gh[VP] = {};
-        auto load = [&](int g, R (&rh)[4], R (&rg)[4]) {
+        now.arrive();
+        if (tile + gridDim.x < total) next.at(tile + gridDim.x), fetch(next, stage ^ 1);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int c = 4 * (g * geom.owners + owner) + j;
-                const bool in = live && c < m.C;
-                rh[j] = in ? *reinterpret_cast<const R*>(h + (long long)c * m.HW) : C4::zero();
-                rg[j] = in ? *reinterpret_cast<const R*>(dy + (long long)c * m.HW) : C4::zero();
-            }
-        };
-        auto dot = [&](int g, const R (&rh)[4], const R (&rg)[4], float (&sum)[4]) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = 4 * (g * geom.owners + owner) + j;
-                if (c >= m.C) continue;
+                const int c = 4 * now.quad(g) + j;
+                if (!now.in(c)) continue;
                 const float w = a.weight[c];
                 float fh[VP], fg[VP];
-                unpack(rh[j], fh);
-                unpack(rg[j], fg);
+                unpack(*now.slot(stage, NT, 0, g, j), fh);
+                unpack(*now.slot(stage, NT, 1, g, j), fg);
 #pragma unroll
                 for (int e = 0; e < VP; ++e) {
                     const float q = fg[e] * fh[e];
                     gh[e] += q * w;
-                    sum[j] += q * r[e];
+                    acc[g][j] += q * r[e];
                 }
             }
-        };
-        if (G) {
-#pragma unroll
-            for (int g = 0; g < GR; ++g) load(g, hr[g], gr[g]);
-#pragma unroll
-            for (int g = 0; g < GR; ++g) dot(g, hr[g], gr[g], acc[g]);
-        } else {
-            for (int g = 0; g < iters; ++g) load(g, hr[0], gr[0]), dot(g, hr[0], gr[0], acc[0]);
         }
-        if (!a.dres && !(DROP && a.dx)) continue;
-        tile_sum<VP>(gh, lp, smem, [&](int, float s) { return s / m.C; });
-        auto out = [&](int g, R (&rh)[4], R (&rg)[4]) {
-            const int quad = g * geom.owners + owner;
+        if (!outputs) continue;
+        tile_sum<VP>(gh, geom.lp, sums, [&](int, float s) { return s / m.C; });
+        bool whole = true;
+        if (DROP && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, now.b);
+#pragma unroll
+        for (int e = 0; e < VP; ++e) gh[e] *= r[e] * r[e];
+        for (int g = 0; g < G; ++g) {
+            const int quad = now.quad(g);
             uint32_t keep = whole ? 0xffffffffu : 0u;
             if (DROP && a.dx && d.mode != WTCONV_DROP_SAMPLE && 4 * quad < m.C)
-                keep = keep_tile<VP>(d, offset, row, b, quad);
-            if (!G) load(g, rh, rg);
+                keep = keep_tile<VP>(d, offset, row, now.b, quad);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = 4 * quad + j;
-                if (!live || c >= m.C) continue;
-                const long long at = (long long)c * m.HW;
+                if (!now.in(c)) continue;
+                const long long at = now.element(c);
                 const float w = a.weight[c];
                 float fh[VP], fg[VP], fe[VP] = {};
-                unpack(rh[j], fh);
-                unpack(rg[j], fg);
-                if (a.dh) unpack(*reinterpret_cast<const R*>(dh + at), fe);
+                unpack(*now.slot(stage, NT, 0, g, j), fh);
+                unpack(*now.slot(stage, NT, 1, g, j), fg);
+                if (a.dh) unpack(*now.slot(stage, NT, 2, g, j), fe);
 #pragma unroll
-                for (int e = 0; e < VP; ++e) fe[e] += r[e] * (fg[e] * w - fh[e] * (gh[e] * r[e] * r[e]));
-                if (a.dres) *reinterpret_cast<R*>(static_cast<T*>(a.dres) + base + at) = C4::from(fe);
+                for (int e = 0; e < VP; ++e) fe[e] += r[e] * (fg[e] * w - fh[e] * gh[e]);
+                if (a.dres) *reinterpret_cast<R*>(static_cast<T*>(a.dres) + at) = Chunk<T, VP>::from(fe);
                 if (DROP && a.dx) {
 #pragma unroll
                     for (int e = 0; e < VP; ++e) fe[e] = keep >> (j * VP + e) & 1 ? fe[e] * d.grown : 0.0f;
-                    *reinterpret_cast<R*>(static_cast<T*>(a.dx) + base + at) = C4::from(fe);
+                    *reinterpret_cast<R*>(static_cast<T*>(a.dx) + at) = Chunk<T, VP>::from(fe);
                 }
             }
-        };
-        if (G) {
-#pragma unroll
-            for (int g = 0; g < GR; ++g) out(g, hr[g], gr[g]);
-        } else {
-            for (int g = 0; g < iters; ++g) out(g, hr[0], gr[0]);
         }
     }
-    if (G && a.dweight) {
+    if (a.dweight) {
         float* part = a.part + (size_t)blockIdx.x * m.C;
 #pragma unroll
-        for (int g = 0; g < GR; ++g)
+        for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float v = acc[g][j];
-                for (int o = 1; o < lp; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-                const int c = 4 * (g * geom.owners + owner) + j;
-                if (pl == 0 && c < m.C) part[c] = v;
+                for (int o = 1; o < geom.lp; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+                const int c = 4 * now.quad(g) + j;
+                if (now.pl == 0 && c < m.C) part[c] = v;
             }
+        }
     }
 }
 
-bool chunked(const MapShape& m, int V, std::initializer_list<const void*> ps, const void* y = nullptr, int ybytes = 1) {
-    if (m.HW % V) return false;
-    for (const void* p : ps)
-        if ((uintptr_t)p % 16) return false;
-    return (uintptr_t)y % ybytes == 0;
+// Launches a kernel on at most `most` CTAs, as many as the SMs hold at once.
+template <typename K, typename A>
+int launch(K kernel, const MapShape& m, const A& a, const MapDrop& d, const PlanesGeom& g, size_t smem, long long most, int sms, cudaStream_t s) {
+    const int threads = g.warps * 32;
+    long long ctas = std::min(m.rows / m.HW * g.tiles, most);
+    if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (ctas > sms) ctas = std::min(ctas, (long long)norm_resident(kernel, threads, smem) * sms);
+    kernel<<<(unsigned)ctas, threads, smem, s>>>(m, a, d, g);
+    return (int)ctas;
 }
 
 template <typename T, int VP, int JOIN, bool Q8>
-void run_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
-    const int wide[2] = {1, 2}, narrow[2] = {1, 4};
-    const PlanesGeom g = planes_geom(m, VP, VP == 1 ? narrow : wide, 2);
-    const long long total = m.rows / m.HW * g.tiles;
-    const unsigned grid = (unsigned)std::min(total, 64LL * sms);
-    const int threads = g.warps * 32, px = g.lp * VP;
-    const int groups = !Q8 ? 0 : g.g || a.group >= m.C ? (m.C + a.group - 1) / a.group : 4 * g.owners / a.group;
-    const size_t smem = (size_t)(g.warps + 1 + groups) * px * 4;
-    switch (g.g) {
-        case 1: wtconv_norm_planes_kernel<T, VP, 1, JOIN, Q8><<<grid, threads, smem, s>>>(m, a, d, g); break;
-        case 2: if constexpr (VP != 1) wtconv_norm_planes_kernel<T, VP, 2, JOIN, Q8><<<grid, threads, smem, s>>>(m, a, d, g); break;
-        case 4: if constexpr (VP == 1) wtconv_norm_planes_kernel<T, VP, 4, JOIN, Q8><<<grid, threads, smem, s>>>(m, a, d, g); break;
-        default: wtconv_norm_planes_kernel<T, VP, 0, JOIN, Q8><<<grid, threads, smem, s>>>(m, a, d, g); break;
-    }
+bool run_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
+    PlanesGeom g;
+    if (!planes_geom(m, VP, sizeof(T), JOIN == kPlain ? 1 : 2, 1 << 20, &g)) return false;
+    const int groups = Q8 ? (m.C + a.group - 1) / a.group : 0;
+    const size_t smem = g.head + (size_t)(g.warps + 1 + groups) * g.lp * VP * 4;
+    if (smem > 225 * 1024) return false;
+    launch(wtconv_norm_planes_kernel<T, VP, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
+    return true;
 }
 
 template <typename T, int VP>
-void pick_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
+bool pick_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     if (a.q8 >= 0)
-        a.residual ? run_fwd<T, VP, kResidual, true>(m, a, d, sms, s) : run_fwd<T, VP, kPlain, true>(m, a, d, sms, s);
-    else if (!a.residual) run_fwd<T, VP, kPlain, false>(m, a, d, sms, s);
-    else if (!d.on) run_fwd<T, VP, kResidual, false>(m, a, d, sms, s);
-    else run_fwd<T, VP, kDropped, false>(m, a, d, sms, s);
+        return a.residual ? run_fwd<T, VP, kResidual, true>(m, a, d, sms, s) : run_fwd<T, VP, kPlain, true>(m, a, d, sms, s);
+    if (!a.residual) return run_fwd<T, VP, kPlain, false>(m, a, d, sms, s);
+    if (!d.on) return run_fwd<T, VP, kResidual, false>(m, a, d, sms, s);
+    return run_fwd<T, VP, kDropped, false>(m, a, d, sms, s);
+}
+
+bool aligned(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if ((uintptr_t)p % 16) return false;
+    return true;
 }
 
 template <typename T>
-void fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
+bool fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     constexpr int V = kVec<T>;
-    if (chunked(m, V, {a.x, a.residual, a.h}, a.y, a.q8 >= 0 ? V : 16)) pick_fwd<T, V>(m, a, d, sms, s);
-    else pick_fwd<T, 1>(m, a, d, sms, s);
+    if (!aligned({a.x, a.residual})) return false;
+    if (m.HW % V == 0 && aligned({a.h}) && (uintptr_t)a.y % (a.q8 >= 0 ? V : 16) == 0) return pick_fwd<T, V>(m, a, d, sms, s);
+    return pick_fwd<T, 1>(m, a, d, sms, s);
 }
 
 template <typename T, int VP, bool DROP>
 int run_bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
-    const int wide[2] = {1, 2}, narrow[2] = {1, 4};
-    const PlanesGeom g = planes_geom(m, VP, VP == 1 ? narrow : wide, 2);
-    const long long total = m.rows / m.HW * g.tiles;
-    const unsigned grid = (unsigned)std::min(total, norm_parts(m, sms));
-    const int threads = g.warps * 32;
-    const size_t smem = (size_t)(g.warps + 1) * g.lp * VP * 4;
-    switch (g.g) {
-        case 1: wtconv_norm_planes_bwd_kernel<T, VP, 1, DROP><<<grid, threads, smem, s>>>(m, a, d, g); break;
-        case 2: if constexpr (VP != 1) wtconv_norm_planes_bwd_kernel<T, VP, 2, DROP><<<grid, threads, smem, s>>>(m, a, d, g); break;
-        case 4: if constexpr (VP == 1) wtconv_norm_planes_bwd_kernel<T, VP, 4, DROP><<<grid, threads, smem, s>>>(m, a, d, g); break;
-        default:
-            if (a.dres || a.dx) wtconv_norm_planes_bwd_kernel<T, VP, 0, DROP><<<grid, threads, smem, s>>>(m, a, d, g);
-            return 0;  // no partial sums
+    PlanesGeom g;
+    if (!planes_geom(m, VP, sizeof(T), a.dh ? 3 : 2, 4, &g)) return 0;
+    const size_t smem = g.head + (size_t)(g.warps + 1) * g.lp * VP * 4;
+    const long long most = norm_parts(m, sms);
+    switch (g.iters) {
+        case 1: return launch(wtconv_norm_planes_bwd_kernel<T, VP, 1, DROP>, m, a, d, g, smem, most, sms, s);
+        case 2: return launch(wtconv_norm_planes_bwd_kernel<T, VP, 2, DROP>, m, a, d, g, smem, most, sms, s);
+        default: return launch(wtconv_norm_planes_bwd_kernel<T, VP, 4, DROP>, m, a, d, g, smem, most, sms, s);
     }
-    return (int)grid;
 }
 
+// The number of partial vectors, or 0 if the map is not one for these kernels.
 template <typename T>
 int bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     constexpr int V = kVec<T>;
-    if (chunked(m, V, {a.h, a.dy, a.dh, a.dres, a.dx}))
+    if (!aligned({a.h, a.dy, a.dh})) return 0;
+    if (m.HW % V == 0 && aligned({a.dres, a.dx}))
         return a.dx ? run_bwd<T, V, true>(m, a, d, sms, s) : run_bwd<T, V, false>(m, a, d, sms, s);
     return a.dx ? run_bwd<T, 1, true>(m, a, d, sms, s) : run_bwd<T, 1, false>(m, a, d, sms, s);
 }
@@ -480,14 +449,14 @@ int bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cuda
 }  // namespace
 
 cudaError_t launch_norm_planes_fwd(const MapShape& m, int dtype, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
-    if (dtype == WTCONV_F32) fwd<float>(m, a, d, sms, s);
-    else fwd<__nv_bfloat16>(m, a, d, sms, s);
-    return cudaGetLastError();
+    if (dtype == WTCONV_F32 ? fwd<float>(m, a, d, sms, s) : fwd<__nv_bfloat16>(m, a, d, sms, s)) return cudaGetLastError();
+    return launch_norm_planes_long_fwd(m, dtype, a, d, sms, s);
 }
 
 cudaError_t launch_norm_planes_bwd(const MapShape& m, int dtype, const NormBwdArgs& a, const MapDrop& d, int sms, int* parts, cudaStream_t s) {
     *parts = dtype == WTCONV_F32 ? bwd<float>(m, a, d, sms, s) : bwd<__nv_bfloat16>(m, a, d, sms, s);
-    return cudaGetLastError();
+    if (*parts) return cudaGetLastError();
+    return a.dres || a.dx ? launch_norm_planes_long_bwd(m, dtype, a, d, sms, s) : cudaSuccess;
 }
 
 }  // namespace wtc

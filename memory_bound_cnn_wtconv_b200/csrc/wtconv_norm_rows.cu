@@ -375,14 +375,6 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
     }
 }
 
-// CTAs of a kernel that an SM holds, asked once for each kernel and block size.
-template <typename K>
-int resident(K kernel, int threads, size_t smem) {
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
-    return n;
-}
-
 bool aligned_to(const void* p, uintptr_t n) { return (uintptr_t)p % n == 0; }
 
 template <typename T, int JOIN, bool Q8>
@@ -395,7 +387,7 @@ void run_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms,
     const RowsGeom g = rows_geom(m, V, vec, least);
     const long long ctas = (m.rows + g.step - 1) / g.step;
     auto go = [&](auto kernel) {
-        const unsigned grid = (unsigned)std::min(ctas, ctas <= 4LL * sms ? ctas : (long long)resident(kernel, g.threads, 0) * sms);
+        const unsigned grid = (unsigned)std::min(ctas, ctas <= 4LL * sms ? ctas : (long long)norm_resident(kernel, g.threads, 0) * sms);
         kernel<<<grid, g.threads, 0, s>>>(m, a, d, g.tpr, vec);
     };
     switch (g.nv) {
@@ -426,7 +418,7 @@ int run_bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, 
     const size_t smem = g.tpr <= 32 && g.threads > 32 && a.dweight ? (size_t)(g.threads / 32) * m.C * 4 : 0;
     const long long most = norm_parts(m, sms);
     auto go = [&](auto kernel, size_t bytes) {
-        const unsigned grid = (unsigned)std::min(std::min(ctas, most), ctas <= 2LL * sms ? ctas : (long long)resident(kernel, g.threads, bytes) * sms);
+        const unsigned grid = (unsigned)std::min(std::min(ctas, most), ctas <= 2LL * sms ? ctas : (long long)norm_resident(kernel, g.threads, bytes) * sms);
         kernel<<<grid, g.threads, bytes, s>>>(m, a, d, g.tpr, vec);
         return (int)grid;
     };
