@@ -22,30 +22,49 @@ constexpr int kThreads = 256;
 // Shorter stretches under one decision go to the rows and planes kernels.
 constexpr long long kLeastSpan = 2048;
 
-template <typename T, bool RES>
-__global__ void __launch_bounds__(kThreads) wtconv_dropout_rows_kernel(MapShape m, DropArgs a, MapDrop d, Divide by_slots, Divide by_hw, int vec) {
-    constexpr int V = kVec<T>;
-    const int slots = (int)by_slots.d;
-    const long long n = m.rows * slots, step = (long long)gridDim.x * kThreads;
+// N channels of a row a thread, the same ones in all its rows: a 16-byte chunk
+// (VEC), or four single values (a warp's four loads then meet in two to four
+// lines).
+template <typename T, bool VEC, bool RES>
+__global__ void __launch_bounds__(kThreads) wtconv_dropout_rows_kernel(MapShape m, DropArgs a, MapDrop d, int slots, Divide by_hw) {
+    constexpr int N = VEC ? kVec<T> : 4;
     const uint32_t offset = drop_offset(d);
-    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-        const long long row = by_slots(i);
-        const int c = (int)(i - row * slots) * V;
-        const long long base = row * m.C;
-        const uint4 x = load_channels(static_cast<const T*>(a.x) + base, c, m.C, vec);
-        uint4 res = make_uint4(0, 0, 0, 0);
-        if (RES) res = load_channels(static_cast<const T*>(a.residual) + base, c, m.C, vec);
-        const long long drow = d.mode == WTCONV_DROP_ELEMENT ? row : by_hw(row);
-        float f[V], r[V];
-        unpack(x, f);
-        unpack(res, r);
+    const int across = min(slots, kThreads), down = kThreads / across;
+    const int k = blockIdx.y * kThreads + threadIdx.x % across, c = k * N, y = threadIdx.x / across;
+    if (k >= slots || y >= down) return;
+    const bool sample = d.mode == WTCONV_DROP_SAMPLE;
+    const long long step = (long long)gridDim.x * down;
+#pragma unroll 2
+    for (long long row = (long long)blockIdx.x * down + y; row < m.rows; row += step) {
+        const long long base = row * m.C + c;
+        const T* x = static_cast<const T*>(a.x) + base;
+        const T* res = static_cast<const T*>(a.residual) + base;
+        T* out = static_cast<T*>(a.y) + base;
+        float f[N], r[N] = {};
+        if constexpr (VEC) {
+            unpack(*reinterpret_cast<const uint4*>(x), f);
+            if (RES) unpack(*reinterpret_cast<const uint4*>(res), r);
+        } else {
 #pragma unroll
-        for (int e = 0; e < V; e += 4) {
-            uint4 u = drop_words(d, offset, drow, d.mode == WTCONV_DROP_SAMPLE ? 0 : (c + e) >> 2);
-            if (d.mode == WTCONV_DROP_SAMPLE) u = make_uint4(u.x, u.x, u.x, u.x);
+            for (int e = 0; e < N; ++e) {
+                f[e] = c + e < m.C ? to_f(x[e]) : 0.0f;
+                if (RES) r[e] = c + e < m.C ? to_f(res[e]) : 0.0f;
+            }
+        }
+        const long long drow = d.mode == WTCONV_DROP_ELEMENT ? row : by_hw(row);
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            uint4 u = drop_words(d, offset, drow, sample ? 0 : (c + e) >> 2);
+            if (sample) u.y = u.z = u.w = u.x;
             drop_add4(d, u, f + e, r + e);
         }
-        store_channels(static_cast<T*>(a.y) + base, c, m.C, vec, pack(r));
+        if constexpr (VEC) {
+            *reinterpret_cast<uint4*>(out) = pack(r);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (c + e < m.C) out[e] = from_f<T>(r[e]);
+        }
     }
 }
 
@@ -63,40 +82,22 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_planes_kernel(MapShap
         const T* res = static_cast<const T*>(a.residual) + base;
         R rx[4], rr[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (4 * quad + j < m.C) {
-                rx[j] = *reinterpret_cast<const R*>(x + (long long)j * m.HW);
-                if (RES) rr[j] = *reinterpret_cast<const R*>(res + (long long)j * m.HW);
-            }
-        uint32_t keep[4] = {};  // bit v: pixel v
-        if (d.mode == WTCONV_DROP_ELEMENT) {
-#pragma unroll
-            for (int v = 0; v < VP; ++v) {
-                const uint4 u = drop_words(d, offset, b * m.HW + p + v, quad);
-                keep[0] |= u.x >= d.thresh ? 1u << v : 0u;
-                keep[1] |= u.y >= d.thresh ? 1u << v : 0u;
-                keep[2] |= u.z >= d.thresh ? 1u << v : 0u;
-                keep[3] |= u.w >= d.thresh ? 1u << v : 0u;
-            }
-        } else {
-            const bool sample = d.mode == WTCONV_DROP_SAMPLE;
-            const uint4 u = drop_words(d, offset, b, sample ? 0 : quad);
-            keep[0] = u.x >= d.thresh ? ~0u : 0u;
-            keep[1] = (sample ? u.x : u.y) >= d.thresh ? ~0u : 0u;
-            keep[2] = (sample ? u.x : u.z) >= d.thresh ? ~0u : 0u;
-            keep[3] = (sample ? u.x : u.w) >= d.thresh ? ~0u : 0u;
+        for (int j = 0; j < 4; ++j) {
+            const bool in = 4 * quad + j < m.C;
+            rx[j] = in ? *reinterpret_cast<const R*>(x + (long long)j * m.HW) : Chunk<T, VP>::zero();
+            if (RES) rr[j] = in ? *reinterpret_cast<const R*>(res + (long long)j * m.HW) : Chunk<T, VP>::zero();
         }
+        float f[4][VP], r[4][VP] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            unpack(rx[j], f[j]);
+            if (RES) unpack(rr[j], r[j]);
+        }
+        drop_add_tile<VP>(d, offset, b * m.HW + p, b, quad, f, r);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (4 * quad + j < m.C) {
-                float f[VP], r[VP] = {};
-                unpack(rx[j], f);
-                if (RES) unpack(rr[j], r);
-#pragma unroll
-                for (int e = 0; e < VP; ++e)
-                    if (keep[j] >> e & 1) r[e] = __fmaf_rn(f[e], d.grown, r[e]);
-                *reinterpret_cast<R*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = Chunk<T, VP>::from(r);
-            }
+            if (4 * quad + j < m.C)
+                *reinterpret_cast<R*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = Chunk<T, VP>::from(r[j]);
     }
 }
 
@@ -165,9 +166,12 @@ void run(const MapShape& m, const DropArgs& a, const MapDrop& d, int sms, cudaSt
         wtconv_dropout_spans_kernel<T, RES><<<grid, kThreads, 0, s>>>(m, a, d, spans, len, vec);
     } else if (m.nhwc) {
         const bool vec = m.C % V == 0 && whole;
-        const int slots = (m.C + V - 1) / V;
-        wtconv_dropout_rows_kernel<T, RES><<<ctas(m.rows * slots), kThreads, 0, s>>>(
-            m, a, d, divide_by(slots, m.rows * slots), divide_by(m.HW, m.rows), vec);
+        const int slots = (m.C + (vec ? V : 4) - 1) / (vec ? V : 4), down = kThreads / std::min(slots, kThreads);
+        const unsigned columns = (slots + kThreads - 1) / kThreads;
+        const dim3 grid((unsigned)std::min((m.rows + down - 1) / down, std::max(1LL, 16LL * sms / columns)), columns);
+        const Divide by_hw = divide_by(m.HW, m.rows);
+        if (vec) wtconv_dropout_rows_kernel<T, true, RES><<<grid, kThreads, 0, s>>>(m, a, d, slots, by_hw);
+        else wtconv_dropout_rows_kernel<T, false, RES><<<grid, kThreads, 0, s>>>(m, a, d, slots, by_hw);
     } else {
         const int quads = (m.C + 3) / 4;
         const Divide by_quads = divide_by(quads, samples * quads);

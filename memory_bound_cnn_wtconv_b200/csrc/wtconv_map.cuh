@@ -136,7 +136,12 @@ __device__ __forceinline__ long long drop_row(const MapDrop& d, const MapShape& 
     return d.mode == WTCONV_DROP_ELEMENT ? n : n / m.HW;
 }
 
-// The random words of channels 4 * quad .. 4 * quad + 3 of one mask row.
+// The random words of channels 4 * quad .. 4 * quad + 3 of mask row (hi, lo).
+// Written so that rows which share quad and hi share the multiplications that
+// the first three rounds owe to them alone.
+__device__ __forceinline__ uint4 drop_words(const MapDrop& d, uint32_t offset, uint32_t lo, uint32_t hi, uint32_t quad) {
+    return philox(quad, lo, hi, offset, d.key);
+}
 __device__ __forceinline__ uint4 drop_words(const MapDrop& d, uint32_t offset, long long row, uint32_t quad) {
     return philox(quad, (uint32_t)row, (uint32_t)((unsigned long long)row >> 32), offset, d.key);
 }
@@ -155,6 +160,89 @@ __device__ __forceinline__ void drop_add4(const MapDrop& d, const uint4& u, cons
     if (u.y >= d.thresh) r[1] = __fmaf_rn(f[1], d.grown, r[1]);
     if (u.z >= d.thresh) r[2] = __fmaf_rn(f[2], d.grown, r[2]);
     if (u.w >= d.thresh) r[3] = __fmaf_rn(f[3], d.grown, r[3]);
+}
+// r + d * f of N pixels of four channels, into r; lo: the first pixel's row,
+// a multiple of N; b: the sample.
+template <int N>
+__device__ __forceinline__ void drop_add_tile(const MapDrop& d, uint32_t offset, long long row, long long b, int quad,
+                                              const float (&f)[4][N], float (&r)[4][N]) {
+    if (d.mode == WTCONV_DROP_ELEMENT) {
+        const uint32_t lo = (uint32_t)row, hi = (uint32_t)((unsigned long long)row >> 32);
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+            const uint4 u = drop_words(d, offset, lo + v, hi, quad);
+            if (u.x >= d.thresh) r[0][v] = __fmaf_rn(f[0][v], d.grown, r[0][v]);
+            if (u.y >= d.thresh) r[1][v] = __fmaf_rn(f[1][v], d.grown, r[1][v]);
+            if (u.z >= d.thresh) r[2][v] = __fmaf_rn(f[2][v], d.grown, r[2][v]);
+            if (u.w >= d.thresh) r[3][v] = __fmaf_rn(f[3][v], d.grown, r[3][v]);
+        }
+    } else {
+        const bool sample = d.mode == WTCONV_DROP_SAMPLE;
+        uint4 u = drop_words(d, offset, b, sample ? 0 : quad);
+        if (sample) u.y = u.z = u.w = u.x;
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+            if (u.x >= d.thresh) r[0][v] = __fmaf_rn(f[0][v], d.grown, r[0][v]);
+            if (u.y >= d.thresh) r[1][v] = __fmaf_rn(f[1][v], d.grown, r[1][v]);
+            if (u.z >= d.thresh) r[2][v] = __fmaf_rn(f[2][v], d.grown, r[2][v]);
+            if (u.w >= d.thresh) r[3][v] = __fmaf_rn(f[3][v], d.grown, r[3][v]);
+        }
+    }
+}
+
+// a * b + c, a * b and a + b of N floats, two at an instruction where N is even.
+template <int N>
+__device__ __forceinline__ void fma_n(const float (&a)[N], const float (&b)[N], float (&c)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const float2 t = __ffma2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), make_float2(c[e], c[e + 1]));
+            c[e] = t.x, c[e + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) c[e] = __fmaf_rn(a[e], b[e], c[e]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void fma_n(const float (&a)[N], float b, float (&c)[N]) {
+    float t[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) t[e] = b;
+    fma_n(a, t, c);
+}
+template <int N>
+__device__ __forceinline__ void mul_n(float (&a)[N], const float (&b)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const float2 t = __fmul2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+            a[e] = t.x, a[e + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) a[e] = __fmul_rn(a[e], b[e]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void mul_n(float (&a)[N], float b) {
+    float t[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) t[e] = b;
+    mul_n(a, t);
+}
+template <int N>
+__device__ __forceinline__ void add_n(float (&a)[N], const float (&b)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const float2 t = __fadd2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+            a[e] = t.x, a[e + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) a[e] = __fadd_rn(a[e], b[e]);
+    }
 }
 
 // n / d of a count: a multiply and a shift below 2^31, else a division.

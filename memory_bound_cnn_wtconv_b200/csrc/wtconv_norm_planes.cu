@@ -42,7 +42,8 @@ struct PlanesGeom {
 // not whole chunks), less where two stages of `tensors` tensors do not leave
 // room for two CTAs on an SM, down to 64 bytes, and then what fits at all.
 // False if nothing does.
-bool planes_geom(const MapShape& m, int VP, int esize, int tensors, int most_iters, PlanesGeom* out) {
+bool planes_geom(const MapShape& m, int VP, int esize, int tensors, PlanesGeom* out) {
+    if ((long long)m.C * m.HW >= 1LL << 31) return false;  // offsets within a sample are 32-bit
     const int quads = (m.C + 3) / 4;
     int lp = VP == 1 ? 32 : 8;
     while (lp < 32 && quads * lp <= 16) lp *= 2;
@@ -52,7 +53,7 @@ bool planes_geom(const MapShape& m, int VP, int esize, int tensors, int most_ite
         const int lanes = 32 / lp;
         g.lp = lp;
         g.iters = 1;
-        while (g.iters < most_iters && (quads + lanes * g.iters - 1) / (lanes * g.iters) > 8) g.iters *= 2;
+        while (g.iters < (VP == 1 ? 4 : 2) && (quads + lanes * g.iters - 1) / (lanes * g.iters) > kMaxWarps) g.iters *= 2;
         g.warps = (quads + lanes * g.iters - 1) / (lanes * g.iters);
         if (g.warps > kMaxWarps) continue;
         g.owners = g.warps * lanes;
@@ -78,6 +79,7 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
+// Where a thread is: its tile, and its channels' places in it.
 template <typename T, int VP>
 struct Tile {
     using R = typename Chunk<T, VP>::type;
@@ -86,38 +88,46 @@ struct Tile {
     const PlanesGeom& geom;
     char* smem;
     int pl, owner;
+    uint32_t own;       // this thread's pixel of its first channel, from the tile's first element on
     long long b;
-    int p0, p;       // first pixel of the tile, of this thread
-    bool live;
+    int p0;             // first pixel of the tile
+    bool live;          // this thread's pixels are the map's
+    long long origin;   // the tile's first element
 
     __device__ __forceinline__ Tile(const MapShape& shape, const PlanesGeom& g, char* s) : m(shape), geom(g), smem(s) {
         const int lane = threadIdx.x % 32;
         pl = lane & (geom.lp - 1);
         owner = (threadIdx.x / 32) * (32 / geom.lp) + lane / geom.lp;
+        own = 4u * owner * m.HW + pl * VP;
     }
     __device__ __forceinline__ void at(long long tile) {
         b = tile / geom.tiles;
         p0 = (int)(tile - b * geom.tiles) * geom.lp * VP;
-        p = p0 + pl * VP;
-        live = p < m.HW;  // with chunks, HW is a multiple of VP
+        live = p0 + pl * VP < m.HW;  // with chunks, HW is a multiple of VP
+        origin = b * m.C * m.HW + p0;
     }
-    __device__ __forceinline__ int quad(int g) const { return g * geom.owners + owner; }
-    __device__ __forceinline__ bool in(int c) const { return live && c < m.C; }
-    // Element (channel c, this thread's pixel) of the map.
-    __device__ __forceinline__ long long element(int c) const { return (b * m.C + c) * m.HW + p; }
+    __device__ __forceinline__ long long row() const { return b * m.HW + p0 + pl * VP; }
+    __device__ __forceinline__ int channel(int g, int j) const { return 4 * (g * geom.owners + owner) + j; }
+    __device__ __forceinline__ bool in(int g, int j) const { return live && channel(g, j) < m.C; }
+    // This thread's chunk of channel(g, j), from the tile's first element on.
+    __device__ __forceinline__ uint32_t offset(int g, int j) const { return own + (uint32_t)(4 * g * geom.owners + j) * m.HW; }
+    __device__ __forceinline__ R* chunk(void* p, int g, int j) const {
+        return reinterpret_cast<R*>(static_cast<T*>(p) + origin + offset(g, j));
+    }
 
-    // This thread's chunk of channel 4 * quad(g) + j of tensor k, in shared memory.
+    // The same of tensor k, in shared memory.
     __device__ __forceinline__ R* slot(int stage, int tensors, int k, int g, int j) const {
         char* s = smem + (stage * tensors + k) * geom.tensor;
         if constexpr (VP == 1) {
-            const int c = 4 * quad(g) + j;
-            const uint32_t first = (uint32_t)((b * m.C + c) * m.HW + p0) * (uint32_t)sizeof(T);  // modulo 2^32
+            const int c = channel(g, j);
+            const uint32_t first = ((uint32_t)origin + (uint32_t)c * m.HW) * (uint32_t)sizeof(T);  // modulo 2^32
             return reinterpret_cast<R*>(s + c * geom.row + (first & 15) + pl * sizeof(T));
         } else {
             return reinterpret_cast<R*>(s) + (4 * g + j) * blockDim.x + threadIdx.x;
         }
     }
     // Starts the copy of tensor k of this tile; with skip, zeros.
+    template <int G>
     __device__ __forceinline__ void fetch(int stage, int tensors, int k, const void* from, bool skip) const {
         if constexpr (VP == 1) {
             const long long bytes = m.rows * m.C * (long long)sizeof(T);
@@ -127,32 +137,34 @@ struct Tile {
             for (int i = threadIdx.x; i < n; i += blockDim.x) {
                 const int c = (int)((__umulhi((uint32_t)i, geom.by_chunks.mul) + (uint32_t)i) >> geom.by_chunks.shift);
                 const int q = i - c * chunks;
-                const long long first = ((b * m.C + c) * m.HW + p0) * (long long)sizeof(T);
+                const long long first = (origin + (uint32_t)c * m.HW) * (long long)sizeof(T);
                 const int span = (int)(first & 15) + pixels * (int)sizeof(T);  // from the chunk boundary on
                 if (16 * q >= span) continue;
                 const long long at = (first & ~15LL) + 16 * q;
                 copy16(s + c * geom.row + 16 * q, static_cast<const char*>(from) + at, skip ? 0 : (int)min(16LL, bytes - at));
             }
         } else {
-            for (int g = 0; g < geom.iters; ++g) {
+            const T* base = static_cast<const T*>(from) + origin;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int c = 4 * quad(g) + j;
-                    const bool ok = in(c) && !skip;
-                    copy16(slot(stage, tensors, k, g, j), static_cast<const T*>(from) + (ok ? element(c) : 0), ok ? 16 : 0);
+                    const bool ok = in(g, j) && !skip;
+                    copy16(slot(stage, tensors, k, g, j), base + (ok ? offset(g, j) : 0u), ok ? 16 : 0);
                 }
             }
         }
     }
-    // The oldest of two stages has arrived (and, where threads read what others
-    // copied, for all of them; their reads of the other stage are over).
+    // A stage has arrived (and, where threads read what others copied, for all
+    // of them; their reads of the other stage are over).
     __device__ __forceinline__ void arrive() const {
         copies_wait<0>();
         if constexpr (VP == 1) __syncthreads();
     }
 };
 
-template <typename T, int VP, int JOIN, bool Q8>
+// G: quads of an owner (geom.iters), at compile time for what stays in registers.
+template <typename T, int VP, int G, int JOIN, bool Q8>
 __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapShape m, NormFwdArgs a, MapDrop d, PlanesGeom geom) {
     using R = typename Chunk<T, VP>::type;
     constexpr int NT = JOIN == kPlain ? 1 : 2;
@@ -165,10 +177,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
     auto fetch = [&](const Tile<T, VP>& t, int stage) {
         bool skip = false;
         if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) skip = !keep_sample(d, offset, t.b);
-        t.fetch(stage, NT, 0, a.x, skip);
-        if (JOIN != kPlain) t.fetch(stage, NT, 1, a.residual, false);
+        t.template fetch<G>(stage, NT, 0, a.x, skip);
+        if (JOIN != kPlain) t.template fetch<G>(stage, NT, 1, a.residual, false);
         copies_commit();
     };
+    float w[G][4];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[g][j] = now.channel(g, j) < m.C ? a.weight[now.channel(g, j)] : 0.0f;
+    }
     next.at(blockIdx.x);
     fetch(next, 0);
     int stage = 0;
@@ -176,36 +194,45 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
         now.at(tile);
         now.arrive();
         if (tile + gridDim.x < total) next.at(tile + gridDim.x), fetch(next, stage ^ 1);
-        const long long row = now.b * m.HW + now.p;
-        bool whole = true;
-        if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, now.b);
+        R h[G][4];
         float ss[VP] = {};
-        for (int g = 0; g < geom.iters; ++g) {
-            const int quad = now.quad(g);
-            uint32_t keep = whole ? 0xffffffffu : 0u;
-            if (JOIN == kDropped && d.mode != WTCONV_DROP_SAMPLE && 4 * quad < m.C)
-                keep = keep_tile<VP>(d, offset, row, now.b, quad);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if (JOIN == kDropped) {
+                float f[4][VP] = {}, r[4][VP] = {};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!now.in(g, j)) continue;
+                    unpack(*now.slot(stage, NT, 0, g, j), f[j]);
+                    unpack(*now.slot(stage, NT, 1, g, j), r[j]);
+                }
+                if (now.in(g, 0)) drop_add_tile<VP>(d, offset, now.row(), now.b, now.channel(g, 0) / 4, f, r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    h[g][j] = Chunk<T, VP>::from(r[j]);
+                    if (now.in(g, j)) *now.chunk(a.h, g, j) = h[g][j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    h[g][j] = Chunk<T, VP>::zero();
+                    if (!now.in(g, j)) continue;
+                    h[g][j] = *now.slot(stage, NT, 0, g, j);
+                    if (JOIN == kResidual) {
+                        float f[VP], r[VP];
+                        unpack(h[g][j], f);
+                        unpack(*now.slot(stage, NT, 1, g, j), r);
+                        add_n(f, r);
+                        h[g][j] = Chunk<T, VP>::from(f);
+                        *now.chunk(a.h, g, j) = h[g][j];
+                    }
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (!now.in(4 * quad + j)) continue;
-                R* at = now.slot(stage, NT, 0, g, j);
                 float f[VP];
-                unpack(*at, f);
-                if (JOIN != kPlain) {
-                    float r[VP];
-                    unpack(*now.slot(stage, NT, 1, g, j), r);
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) {
-                        if (JOIN != kDropped) r[e] += f[e];
-                        else if (keep >> (j * VP + e) & 1) r[e] = __fmaf_rn(f[e], d.grown, r[e]);
-                    }
-                    const R h = Chunk<T, VP>::from(r);
-                    *reinterpret_cast<R*>(static_cast<T*>(a.h) + now.element(4 * quad + j)) = h;
-                    *at = h;
-                    unpack(h, f);  // the norm is of h as it is stored
-                }
-#pragma unroll
-                for (int e = 0; e < VP; ++e) ss[e] += f[e] * f[e];
+                unpack(h[g][j], f);  // the norm is of h as it is stored
+                fma_n(f, f, ss);
             }
         }
         tile_sum<VP>(ss, geom.lp, sums, [&](int q, float s) {
@@ -213,22 +240,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
             if (a.rstd && now.p0 + q < m.HW) a.rstd[now.b * m.HW + now.p0 + q] = r;
             return r;
         });
-        // v = h * r * w of channel c
-        auto value = [&](int g, int j, int c, float (&f)[VP]) {
-            const float w = a.weight[c];
-            unpack(*now.slot(stage, NT, 0, g, j), f);
-#pragma unroll
-            for (int e = 0; e < VP; ++e) f[e] = f[e] * ss[e] * w;
+        // v = h * r * w
+        auto value = [&](int g, int j, float (&f)[VP]) {
+            unpack(h[g][j], f);
+            mul_n(f, ss);
+            mul_n(f, w[g][j]);
         };
         if (!Q8) {
-            for (int g = 0; g < geom.iters; ++g) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int c = 4 * now.quad(g) + j;
-                    if (!now.in(c)) continue;
+                    if (!now.in(g, j)) continue;
                     float f[VP];
-                    value(g, j, c, f);
-                    *reinterpret_cast<R*>(static_cast<T*>(a.y) + now.element(c)) = Chunk<T, VP>::from(f);
+                    value(g, j, f);
+                    *now.chunk(a.y, g, j) = Chunk<T, VP>::from(f);
                 }
             }
         } else {
@@ -236,45 +262,42 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
             const int groups = (m.C + a.group - 1) / a.group;
             for (int q = threadIdx.x; q < groups * px; q += blockDim.x) top[q] = 0;
             __syncthreads();
-            for (int g = 0; g < geom.iters; ++g) {
-                const int c0 = 4 * now.quad(g);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
                 uint32_t bits[VP] = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (!now.in(c0 + j)) continue;
                     float f[VP];
-                    value(g, j, c0 + j, f);
+                    value(g, j, f);  // 0 past the last channel
 #pragma unroll
                     for (int e = 0; e < VP; ++e) bits[e] = max(bits[e], abs_bits(f[e]));
                 }
-                if (now.in(c0)) {
+                if (now.in(g, 0)) {
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) atomicMax(&top[c0 / a.group * px + now.pl * VP + e], bits[e]);
+                    for (int e = 0; e < VP; ++e) atomicMax(&top[now.channel(g, 0) / a.group * px + now.pl * VP + e], bits[e]);
                 }
             }
             __syncthreads();
             for (int q = threadIdx.x; q < groups * px; q += blockDim.x) {
                 const float s = q8_scale(top[q], a.q8);
                 top[q] = __float_as_uint(1.0f / s);  // one rounding more than v / scale
-                const int pixel = now.p0 + q % px;
-                if (pixel < m.HW) a.scale[(now.b * groups + q / px) * m.HW + pixel] = s;
+                const int gr = q / px, pixel = now.p0 + q - gr * px;
+                if (pixel < m.HW) a.scale[(now.b * groups + gr) * m.HW + pixel] = s;
             }
             __syncthreads();
-            for (int g = 0; g < geom.iters; ++g) {
-                const int c0 = 4 * now.quad(g);
-                float inv[VP];
-                if (c0 < m.C) {
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) inv[e] = __uint_as_float(top[c0 / a.group * px + now.pl * VP + e]);
-                }
+            for (int g = 0; g < G; ++g) {
+                if (!now.in(g, 0)) continue;
+                float inv[VP];
+#pragma unroll
+                for (int e = 0; e < VP; ++e) inv[e] = __uint_as_float(top[now.channel(g, 0) / a.group * px + now.pl * VP + e]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (!now.in(c0 + j)) continue;
+                    if (!now.in(g, j)) continue;
                     float f[VP];
-                    value(g, j, c0 + j, f);
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) f[e] *= inv[e];
-                    q8_store<VP>(static_cast<uint8_t*>(a.y) + now.element(c0 + j), f, a.q8);
+                    value(g, j, f);
+                    mul_n(f, inv);
+                    q8_store<VP>(static_cast<uint8_t*>(a.y) + now.origin + now.offset(g, j), f, a.q8);
                 }
             }
             __syncthreads();  // before the next tile clears `top`
@@ -282,7 +305,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
     }
 }
 
-// G: quads of an owner (geom.iters), at compile time for the sums in registers.
 template <typename T, int VP, int G, bool DROP>
 __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(MapShape m, NormBwdArgs a, MapDrop d, PlanesGeom geom) {
     using R = typename Chunk<T, VP>::type;
@@ -294,22 +316,26 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
     const bool outputs = a.dres || (DROP && a.dx);
     Tile<T, VP> now(m, geom, smem), next(m, geom, smem);
     auto fetch = [&](const Tile<T, VP>& t, int stage) {
-        t.fetch(stage, NT, 0, a.h, false);
-        t.fetch(stage, NT, 1, a.dy, false);
-        if (a.dh) t.fetch(stage, NT, 2, a.dh, false);
+        t.template fetch<G>(stage, NT, 0, a.h, false);
+        t.template fetch<G>(stage, NT, 1, a.dy, false);
+        if (a.dh) t.template fetch<G>(stage, NT, 2, a.dh, false);
         copies_commit();
     };
-    float acc[G][4] = {};
+    float w[G][4], acc[G][4] = {};
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[g][j] = now.channel(g, j) < m.C ? a.weight[now.channel(g, j)] : 0.0f;
+    }
     next.at(blockIdx.x);
     fetch(next, 0);
     int stage = 0;
     for (long long tile = blockIdx.x; tile < total; tile += gridDim.x, stage ^= 1) {
         now.at(tile);
         float r[VP] = {}, gh[VP] = {};
-        const long long row = now.b * m.HW + now.p;
         if (now.live) {
 #pragma unroll
-            for (int e = 0; e < VP; ++e) r[e] = a.rstd[row + e];
+            for (int e = 0; e < VP; ++e) r[e] = a.rstd[now.row() + e];
         }
         now.arrive();
         if (tile + gridDim.x < total) next.at(tile + gridDim.x), fetch(next, stage ^ 1);
@@ -317,49 +343,50 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
         for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int c = 4 * now.quad(g) + j;
-                if (!now.in(c)) continue;
-                const float w = a.weight[c];
-                float fh[VP], fg[VP];
+                if (!now.in(g, j)) continue;
+                float fh[VP], fg[VP], own[VP] = {};
                 unpack(*now.slot(stage, NT, 0, g, j), fh);
                 unpack(*now.slot(stage, NT, 1, g, j), fg);
+                mul_n(fg, fh);
+                fma_n(fg, w[g][j], gh);
+                fma_n(fg, r, own);
 #pragma unroll
-                for (int e = 0; e < VP; ++e) {
-                    const float q = fg[e] * fh[e];
-                    gh[e] += q * w;
-                    acc[g][j] += q * r[e];
-                }
+                for (int e = 0; e < VP; ++e) acc[g][j] += own[e];
             }
         }
         if (!outputs) continue;
         tile_sum<VP>(gh, geom.lp, sums, [&](int, float s) { return s / m.C; });
         bool whole = true;
         if (DROP && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, now.b);
+        // dres = dh + (r * w) * dy - (r^3 mean(g * h)) * h
 #pragma unroll
-        for (int e = 0; e < VP; ++e) gh[e] *= r[e] * r[e];
+        for (int e = 0; e < VP; ++e) gh[e] *= -(r[e] * r[e] * r[e]);
+#pragma unroll
         for (int g = 0; g < G; ++g) {
-            const int quad = now.quad(g);
-            uint32_t keep = whole ? 0xffffffffu : 0u;
-            if (DROP && a.dx && d.mode != WTCONV_DROP_SAMPLE && 4 * quad < m.C)
-                keep = keep_tile<VP>(d, offset, row, now.b, quad);
+            float fe[4][VP] = {};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int c = 4 * quad + j;
-                if (!now.in(c)) continue;
-                const long long at = now.element(c);
-                const float w = a.weight[c];
-                float fh[VP], fg[VP], fe[VP] = {};
+                if (!now.in(g, j)) continue;
+                float fh[VP], fg[VP];
                 unpack(*now.slot(stage, NT, 0, g, j), fh);
                 unpack(*now.slot(stage, NT, 1, g, j), fg);
-                if (a.dh) unpack(*now.slot(stage, NT, 2, g, j), fe);
+                if (a.dh) unpack(*now.slot(stage, NT, 2, g, j), fe[j]);
+                mul_n(fg, w[g][j]);
+                fma_n(fg, r, fe[j]);
+                fma_n(fh, gh, fe[j]);
+                if (a.dres) *now.chunk(a.dres, g, j) = Chunk<T, VP>::from(fe[j]);
+            }
+            if (DROP && a.dx) {
+                float dx[4][VP] = {};
+                if (d.mode != WTCONV_DROP_SAMPLE) {
+                    if (now.in(g, 0)) drop_add_tile<VP>(d, offset, now.row(), now.b, now.channel(g, 0) / 4, fe, dx);
+                } else if (whole) {
 #pragma unroll
-                for (int e = 0; e < VP; ++e) fe[e] += r[e] * (fg[e] * w - fh[e] * gh[e]);
-                if (a.dres) *reinterpret_cast<R*>(static_cast<T*>(a.dres) + at) = Chunk<T, VP>::from(fe);
-                if (DROP && a.dx) {
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) fe[e] = keep >> (j * VP + e) & 1 ? fe[e] * d.grown : 0.0f;
-                    *reinterpret_cast<R*>(static_cast<T*>(a.dx) + at) = Chunk<T, VP>::from(fe);
+                    for (int j = 0; j < 4; ++j) fma_n(fe[j], d.grown, dx[j]);
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (now.in(g, j)) *now.chunk(a.dx, g, j) = Chunk<T, VP>::from(dx[j]);
             }
         }
     }
@@ -371,7 +398,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
             for (int j = 0; j < 4; ++j) {
                 float v = acc[g][j];
                 for (int o = 1; o < geom.lp; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-                const int c = 4 * now.quad(g) + j;
+                const int c = now.channel(g, j);
                 if (now.pl == 0 && c < m.C) part[c] = v;
             }
         }
@@ -392,11 +419,16 @@ int launch(K kernel, const MapShape& m, const A& a, const MapDrop& d, const Plan
 template <typename T, int VP, int JOIN, bool Q8>
 bool run_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     PlanesGeom g;
-    if (!planes_geom(m, VP, sizeof(T), JOIN == kPlain ? 1 : 2, 1 << 20, &g)) return false;
+    if (!planes_geom(m, VP, sizeof(T), JOIN == kPlain ? 1 : 2, &g)) return false;
     const int groups = Q8 ? (m.C + a.group - 1) / a.group : 0;
     const size_t smem = g.head + (size_t)(g.warps + 1 + groups) * g.lp * VP * 4;
     if (smem > 225 * 1024) return false;
-    launch(wtconv_norm_planes_kernel<T, VP, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
+    switch (g.iters) {
+        case 1: launch(wtconv_norm_planes_kernel<T, VP, 1, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s); break;
+        case 2: launch(wtconv_norm_planes_kernel<T, VP, 2, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s); break;
+        default:
+            if constexpr (VP == 1) launch(wtconv_norm_planes_kernel<T, VP, 4, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
+    }
     return true;
 }
 
@@ -426,14 +458,16 @@ bool fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cud
 template <typename T, int VP, bool DROP>
 int run_bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     PlanesGeom g;
-    if (!planes_geom(m, VP, sizeof(T), a.dh ? 3 : 2, 4, &g)) return 0;
+    if (!planes_geom(m, VP, sizeof(T), a.dh ? 3 : 2, &g)) return 0;
     const size_t smem = g.head + (size_t)(g.warps + 1) * g.lp * VP * 4;
     const long long most = norm_parts(m, sms);
     switch (g.iters) {
         case 1: return launch(wtconv_norm_planes_bwd_kernel<T, VP, 1, DROP>, m, a, d, g, smem, most, sms, s);
         case 2: return launch(wtconv_norm_planes_bwd_kernel<T, VP, 2, DROP>, m, a, d, g, smem, most, sms, s);
-        default: return launch(wtconv_norm_planes_bwd_kernel<T, VP, 4, DROP>, m, a, d, g, smem, most, sms, s);
+        default:
+            if constexpr (VP == 1) return launch(wtconv_norm_planes_bwd_kernel<T, VP, 4, DROP>, m, a, d, g, smem, most, sms, s);
     }
+    return 0;
 }
 
 // The number of partial vectors, or 0 if the map is not one for these kernels.
