@@ -83,29 +83,6 @@ struct Chunk<T, 1> {
     static __device__ __forceinline__ T from(const float (&f)[1]) { return from_f<T>(f[0]); }
 };
 
-// The chunk of channels c .. c + V - 1 of a row at p (16 bytes at once with
-// vec; else one by one, channels past C as zeros).
-template <typename T>
-__device__ __forceinline__ uint4 load_channels(const T* p, int c, int C, bool vec) {
-    if (vec) return *reinterpret_cast<const uint4*>(p + c);
-    float f[kVec<T>];
-#pragma unroll
-    for (int e = 0; e < kVec<T>; ++e) f[e] = c + e < C ? to_f(p[c + e]) : 0.0f;
-    return pack(f);
-}
-template <typename T>
-__device__ __forceinline__ void store_channels(T* p, int c, int C, bool vec, const uint4& r) {
-    if (vec) {
-        *reinterpret_cast<uint4*>(p + c) = r;
-        return;
-    }
-    float f[kVec<T>];
-    unpack(r, f);
-#pragma unroll
-    for (int e = 0; e < kVec<T>; ++e)
-        if (c + e < C) p[c + e] = from_f<T>(f[e]);
-}
-
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as
 // easy as 1, 2, 3", 2011): four random words from a 128-bit counter and a
 // 64-bit key, whose ten round keys come ready made.
