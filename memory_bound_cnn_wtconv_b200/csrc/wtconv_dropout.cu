@@ -26,7 +26,7 @@ constexpr long long kLeastSpan = 2048;
 // (VEC), or four single values (a warp's four loads then meet in two to four
 // lines).
 template <typename T, bool VEC, bool RES>
-__global__ void __launch_bounds__(kThreads) wtconv_dropout_rows_kernel(MapShape m, DropArgs a, MapDrop d, int slots, Divide by_hw) {
+__global__ void __launch_bounds__(kThreads) wtconv_dropout_rows_kernel(MapShape m, DropArgs a, MapDrop d, int slots) {
     constexpr int N = VEC ? kVec<T> : 4;
     const uint32_t offset = drop_offset(d);
     const int across = min(slots, kThreads), down = kThreads / across;
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_rows_kernel(MapShape 
                 if (RES) r[e] = c + e < m.C ? to_f(res[e]) : 0.0f;
             }
         }
-        const long long drow = d.mode == WTCONV_DROP_ELEMENT ? row : by_hw(row);
+        const long long drow = drop_row(d, row);
 #pragma unroll
         for (int e = 0; e < N; e += 4) {
             uint4 u = drop_words(d, offset, drow, sample ? 0 : (c + e) >> 2);
@@ -169,9 +169,8 @@ void run(const MapShape& m, const DropArgs& a, const MapDrop& d, int sms, cudaSt
         const int slots = (m.C + (vec ? V : 4) - 1) / (vec ? V : 4), down = kThreads / std::min(slots, kThreads);
         const unsigned columns = (slots + kThreads - 1) / kThreads;
         const dim3 grid((unsigned)std::min((m.rows + down - 1) / down, std::max(1LL, 16LL * sms / columns)), columns);
-        const Divide by_hw = divide_by(m.HW, m.rows);
-        if (vec) wtconv_dropout_rows_kernel<T, true, RES><<<grid, kThreads, 0, s>>>(m, a, d, slots, by_hw);
-        else wtconv_dropout_rows_kernel<T, false, RES><<<grid, kThreads, 0, s>>>(m, a, d, slots, by_hw);
+        if (vec) wtconv_dropout_rows_kernel<T, true, RES><<<grid, kThreads, 0, s>>>(m, a, d, slots);
+        else wtconv_dropout_rows_kernel<T, false, RES><<<grid, kThreads, 0, s>>>(m, a, d, slots);
     } else {
         const int quads = (m.C + 3) / 4;
         const Divide by_quads = divide_by(quads, samples * quads);

@@ -20,6 +20,23 @@ struct MapShape {
     int nhwc;        // 1: the C values of a row are adjacent
 };
 
+// n / d of a count: a multiply and a shift below 2^31, else a division.
+struct Divide {
+    FastDiv f;
+    long long d;
+    int small;  // every n is below 2^31
+    __device__ __forceinline__ long long operator()(long long n) const {
+        return small ? (long long)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift) : n / d;
+    }
+};
+inline Divide divide_by(long long d, long long most) {
+    Divide v{};
+    v.d = d;
+    v.small = most < (1LL << 31) && d < (1LL << 31);
+    if (v.small) v.f = make_fastdiv((uint32_t)d);
+    return v;
+}
+
 // Dropout of one call.  Nothing is dropped when `on` is 0.
 struct MapDrop {
     uint32_t thresh;                // dropped where the random word is below this
@@ -29,6 +46,7 @@ struct MapDrop {
     const long long* offset_dev;    // added to offset if not NULL (read by the kernel: a replayed graph sees its value)
     int mode;                       // wtconv_drop_mode_t
     int on;
+    Divide by_hw;                   // a row's sample
 };
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -109,8 +127,8 @@ __device__ __forceinline__ uint32_t drop_offset(const MapDrop& d) {
 }
 
 // The mask's row: the pixel (element), or the sample (channel, sample).
-__device__ __forceinline__ long long drop_row(const MapDrop& d, const MapShape& m, long long n) {
-    return d.mode == WTCONV_DROP_ELEMENT ? n : n / m.HW;
+__device__ __forceinline__ long long drop_row(const MapDrop& d, long long n) {
+    return d.mode == WTCONV_DROP_ELEMENT ? n : d.by_hw(n);
 }
 
 // The random words of channels 4 * quad .. 4 * quad + 3 of mask row (hi, lo).
@@ -220,23 +238,6 @@ __device__ __forceinline__ void add_n(float (&a)[N], const float (&b)[N]) {
 #pragma unroll
         for (int e = 0; e < N; ++e) a[e] = __fadd_rn(a[e], b[e]);
     }
-}
-
-// n / d of a count: a multiply and a shift below 2^31, else a division.
-struct Divide {
-    FastDiv f;
-    long long d;
-    int small;  // every n is below 2^31
-    __device__ __forceinline__ long long operator()(long long n) const {
-        return small ? (long long)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift) : n / d;
-    }
-};
-inline Divide divide_by(long long d, long long most) {
-    Divide v{};
-    v.d = d;
-    v.small = most < (1LL << 31) && d < (1LL << 31);
-    if (v.small) v.f = make_fastdiv((uint32_t)d);
-    return v;
 }
 
 }  // namespace wtc

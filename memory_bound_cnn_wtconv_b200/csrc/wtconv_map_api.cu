@@ -41,7 +41,7 @@ wtconv_status_t map_shape(const wtconv_map_desc_t* d, MapShape* m) {
     return WTCONV_OK;
 }
 
-wtconv_status_t map_drop(const wtconv_drop_t* p, MapDrop* d) {
+wtconv_status_t map_drop(const wtconv_drop_t* p, const MapShape& m, MapDrop* d) {
     memset(d, 0, sizeof(*d));
     d->grown = 1.0f;
     if (!p) return WTCONV_OK;
@@ -54,6 +54,7 @@ wtconv_status_t map_drop(const wtconv_drop_t* p, MapDrop* d) {
     d->offset = (uint32_t)p->offset;
     d->offset_dev = (const long long*)p->offset_dev;
     d->mode = p->mode;
+    d->by_hw = divide_by(m.HW, m.rows);
     d->on = d->thresh != 0;
     return WTCONV_OK;
 }
@@ -91,7 +92,7 @@ wtconv_status_t norm_forward(const wtconv_map_desc_t* d, float eps, const void* 
     if (st != WTCONV_OK) return st;
     if (!(eps > 0.0f) || isinf(eps)) return WTCONV_ERR_ARGUMENT;
     MapDrop md;
-    st = map_drop(drop, &md);
+    st = map_drop(drop, m, &md);
     if (st != WTCONV_OK) return st;
     if (m.rows == 0) return WTCONV_OK;  // nothing to do, whatever the (empty) buffers' addresses
     if (drop && !residual) return WTCONV_ERR_ARGUMENT;
@@ -125,7 +126,7 @@ wtconv_status_t wtconv_dropout(const wtconv_map_desc_t* d, const wtconv_drop_t* 
     if (st != WTCONV_OK) return st;
     if (!drop) return WTCONV_ERR_NULLPTR;
     MapDrop md;
-    st = map_drop(drop, &md);
+    st = map_drop(drop, m, &md);
     if (st != WTCONV_OK) return st;
     if (m.rows == 0) return WTCONV_OK;
     if (!x || !y) return WTCONV_ERR_NULLPTR;
@@ -169,7 +170,7 @@ wtconv_status_t wtconv_rms_norm_backward(const wtconv_map_desc_t* d, const void*
     wtconv_status_t st = map_shape(d, &m);
     if (st != WTCONV_OK) return st;
     MapDrop md;
-    st = map_drop(drop, &md);
+    st = map_drop(drop, m, &md);
     if (st != WTCONV_OK) return st;
     if (dx && !drop) return WTCONV_ERR_ARGUMENT;
     if (m.rows == 0) {

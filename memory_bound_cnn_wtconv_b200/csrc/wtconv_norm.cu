@@ -17,19 +17,25 @@ namespace wtc {
 
 namespace {
 
-// The partial vectors' sum: 32 channels a CTA, 32 threads to a channel, each
-// with every 32nd vector, then the 32 in order.
+// The partial vectors' sum: 8 channels a CTA, 128 threads to a channel, each
+// with every 128th vector (a few loads in flight at once), then the 128 in a
+// fixed order.  Launched to start while the kernel before it ends.
 __global__ void __launch_bounds__(1024) wtconv_norm_finish_kernel(int C, int parts, const float* part, float* dweight) {
-    __shared__ float sums[32][33];
-    const int c = blockIdx.x * 32 + threadIdx.x;
+    __shared__ float sums[8][129];
+    const int x = threadIdx.x % 8, y = threadIdx.x / 8, c = blockIdx.x * 8 + x;
+    cudaGridDependencySynchronize();
     float v = 0.0f;
-    if (c < C)
-        for (int k = threadIdx.y; k < parts; k += 32) v += part[(size_t)k * C + c];
-    sums[threadIdx.y][threadIdx.x] = v;
+    if (c < C) {
+#pragma unroll 8
+        for (int k = y; k < parts; k += 128) v += part[(size_t)k * C + c];
+    }
+    sums[x][y] = v;
     __syncthreads();
-    v = sums[threadIdx.x][threadIdx.y];
+    if (threadIdx.x >= 256) return;
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+    v = sums[w][lane] + sums[w][lane + 32] + sums[w][lane + 64] + sums[w][lane + 96];
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (threadIdx.x == 0 && blockIdx.x * 32 + threadIdx.y < C) dweight[blockIdx.x * 32 + threadIdx.y] = v;
+    if (lane == 0 && blockIdx.x * 8 + w < C) dweight[blockIdx.x * 8 + w] = v;
 }
 
 // Partial sums where a CTA's registers do not hold a row (so there are many
@@ -77,8 +83,16 @@ cudaError_t launch_norm_bwd(const MapShape& m, int dtype, const NormBwdArgs& a, 
         if (dtype == WTCONV_F32) wtconv_norm_columns_kernel<float><<<grid, 256, 0, s>>>(m, a);
         else wtconv_norm_columns_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(m, a);
     }
-    wtconv_norm_finish_kernel<<<(m.C + 31) / 32, dim3(32, 32), 0, s>>>(m.C, parts, a.part, a.dweight);
-    return cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3((m.C + 7) / 8);
+    config.blockDim = dim3(1024);
+    config.stream = s;
+    config.attrs = &early;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, wtconv_norm_finish_kernel, m.C, parts, (const float*)a.part, a.dweight);
 }
 
 }  // namespace wtc

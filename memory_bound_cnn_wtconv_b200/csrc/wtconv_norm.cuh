@@ -49,6 +49,11 @@ __device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d,
     return r;
 }
 
+__device__ __forceinline__ uint8_t q8_one(float v, int q8) {
+    if (q8 == WTCONV_E4M3) return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+    return (uint8_t)(isnan(v) ? 0 : max(-127, min(127, __float2int_rn(v))));
+}
+
 // |v| as bits that are ordered like |v|, NaN above infinity.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 

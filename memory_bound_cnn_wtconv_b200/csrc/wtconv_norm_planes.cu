@@ -8,9 +8,10 @@
 // The inputs of the next tile come into shared memory (cp.async, 16 bytes)
 // while this one is computed.  VP = 16 bytes of pixels where planes are whole
 // 16-byte chunks: each thread copies the chunks that it owns itself, so nothing
-// but its own copies has to arrive.  VP = 1 where they are not: each channel's
-// pixels come as the aligned chunks that cover them, shifted by the plane's own
-// distance from a 16-byte boundary, and are read value by value.
+// but its own copies has to arrive.  Where they are not (RAG, "ragged"), each
+// channel's pixels come as the aligned chunks that cover them, shifted by the
+// plane's own distance from a 16-byte boundary, and are read value by value: a
+// thread then has the pixels pl, pl + lp, ..., four of them.
 //
 // Bound by memory.  Without the copies ahead a CTA loads, waits, sums and
 // stores in turn, and too few CTAs fit an SM to hide it: 388 us for the
@@ -29,23 +30,26 @@ constexpr int kMaxWarps = 16;
 constexpr int kSmem = 200 * 1024;      // of the 227 KB a CTA may have
 constexpr int kSmemTwo = 110 * 1024;   // two CTAs an SM
 
+constexpr int kRagged = 4;  // pixels of a thread where planes are ragged
+
 struct PlanesGeom {
     int lp, warps, owners, iters;  // iters: quads of an owner
     int tiles;                     // of a plane
-    int row;                       // VP = 1: bytes of a channel's pixels in a stage
+    int row;                       // ragged: bytes of a channel's pixels in a stage
     int tensor;                    // bytes of one tensor in a stage
     int head;                      // bytes of both stages
-    FastDiv by_chunks;             // VP = 1: row / 16
+    FastDiv by_chunks;             // ragged: row / 16
+    Divide by_tiles;
 };
 
-// Tiles of 128 bytes of a plane (all 32 lanes' single values where planes are
-// not whole chunks), less where two stages of `tensors` tensors do not leave
-// room for two CTAs on an SM, down to 64 bytes, and then what fits at all.
-// False if nothing does.
-bool planes_geom(const MapShape& m, int VP, int esize, int tensors, PlanesGeom* out) {
+// Tiles of 128 bytes of a plane (256 where it is ragged, so that the chunks at
+// their ends weigh less), less where two stages of `tensors` tensors do not
+// leave room for two CTAs on an SM, down to 64 bytes, and then what fits at
+// all.  False if nothing does.
+bool planes_geom(const MapShape& m, int VP, bool ragged, int esize, int tensors, PlanesGeom* out) {
     if ((long long)m.C * m.HW >= 1LL << 31) return false;  // offsets within a sample are 32-bit
     const int quads = (m.C + 3) / 4;
-    int lp = VP == 1 ? 32 : 8;
+    int lp = ragged ? 64 / esize : 8;
     while (lp < 32 && quads * lp <= 16) lp *= 2;
     while (lp > 1 && lp / 2 * VP >= m.HW) lp /= 2;
     for (; lp >= 1; lp /= 2) {
@@ -53,18 +57,19 @@ bool planes_geom(const MapShape& m, int VP, int esize, int tensors, PlanesGeom* 
         const int lanes = 32 / lp;
         g.lp = lp;
         g.iters = 1;
-        while (g.iters < (VP == 1 ? 4 : 2) && (quads + lanes * g.iters - 1) / (lanes * g.iters) > kMaxWarps) g.iters *= 2;
+        while (g.iters < 2 && (quads + lanes * g.iters - 1) / (lanes * g.iters) > kMaxWarps) g.iters *= 2;
         g.warps = (quads + lanes * g.iters - 1) / (lanes * g.iters);
         if (g.warps > kMaxWarps) continue;
         g.owners = g.warps * lanes;
         g.tiles = (m.HW + lp * VP - 1) / (lp * VP);
-        g.row = (lp * esize + 15) / 16 * 16 + 16;
-        const long long tensor = VP == 1 ? (long long)g.row * m.C : 64LL * g.iters * g.warps * 32;
+        g.row = (lp * VP * esize + 15) / 16 * 16 + 16;
+        const long long tensor = ragged ? (long long)g.row * m.C : 64LL * g.iters * g.warps * 32;
         if (2 * tensors * tensor > kSmem) continue;
-        if (2 * tensors * tensor > kSmemTwo && lp > (VP == 1 ? 16 : 4)) continue;
+        if (2 * tensors * tensor > kSmemTwo && lp * VP * esize > 64) continue;
         g.tensor = (int)tensor;
         g.head = (int)(2 * tensors * tensor);
         g.by_chunks = make_fastdiv(g.row / 16);
+        g.by_tiles = divide_by(g.tiles, m.rows);
         *out = g;
         return true;
     }
@@ -80,7 +85,7 @@ template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
 // Where a thread is: its tile, and its channels' places in it.
-template <typename T, int VP>
+template <typename T, int VP, bool RAG>
 struct Tile {
     using R = typename Chunk<T, VP>::type;
 
@@ -88,51 +93,82 @@ struct Tile {
     const PlanesGeom& geom;
     char* smem;
     int pl, owner;
-    uint32_t own;       // this thread's pixel of its first channel, from the tile's first element on
+    uint32_t own;       // this thread's first pixel of its first channel, from the tile's first element on
     long long b;
     int p0;             // first pixel of the tile
-    bool live;          // this thread's pixels are the map's
+    int live;           // how many of this thread's pixels are the map's
     long long origin;   // the tile's first element
 
     __device__ __forceinline__ Tile(const MapShape& shape, const PlanesGeom& g, char* s) : m(shape), geom(g), smem(s) {
         const int lane = threadIdx.x % 32;
         pl = lane & (geom.lp - 1);
         owner = (threadIdx.x / 32) * (32 / geom.lp) + lane / geom.lp;
-        own = 4u * owner * m.HW + pl * VP;
+        own = 4u * owner * m.HW + pixel(0);
     }
+    // The tile's pixel that is this thread's e-th.
+    __device__ __forceinline__ int pixel(int e) const { return RAG ? pl + e * geom.lp : pl * VP + e; }
     __device__ __forceinline__ void at(long long tile) {
-        b = tile / geom.tiles;
+        b = geom.by_tiles(tile);
         p0 = (int)(tile - b * geom.tiles) * geom.lp * VP;
-        live = p0 + pl * VP < m.HW;  // with chunks, HW is a multiple of VP
         origin = b * m.C * m.HW + p0;
+        const int left = m.HW - p0 - pixel(0);  // chunks: HW is a multiple of VP
+        live = !RAG ? (left > 0 ? VP : 0) : left <= 0 ? 0 : min(VP, (left - 1) / geom.lp + 1);
     }
-    __device__ __forceinline__ long long row() const { return b * m.HW + p0 + pl * VP; }
+    __device__ __forceinline__ bool has(int e) const { return RAG ? e < live : true; }
+    __device__ __forceinline__ long long row() const { return b * m.HW + p0 + pixel(0); }
     __device__ __forceinline__ int channel(int g, int j) const { return 4 * (g * geom.owners + owner) + j; }
     __device__ __forceinline__ bool in(int g, int j) const { return live && channel(g, j) < m.C; }
-    // This thread's chunk of channel(g, j), from the tile's first element on.
+    // This thread's first pixel of channel(g, j), from the tile's first element on.
     __device__ __forceinline__ uint32_t offset(int g, int j) const { return own + (uint32_t)(4 * g * geom.owners + j) * m.HW; }
-    __device__ __forceinline__ R* chunk(void* p, int g, int j) const {
-        return reinterpret_cast<R*>(static_cast<T*>(p) + origin + offset(g, j));
-    }
 
-    // The same of tensor k, in shared memory.
-    __device__ __forceinline__ R* slot(int stage, int tensors, int k, int g, int j) const {
-        char* s = smem + (stage * tensors + k) * geom.tensor;
-        if constexpr (VP == 1) {
+    // This thread's pixels of channel(g, j) of tensor k of a stage, as floats.
+    __device__ __forceinline__ void load(int stage, int tensors, int k, int g, int j, float (&f)[VP]) const {
+        const char* s = smem + (stage * tensors + k) * geom.tensor;
+        if constexpr (RAG) {
             const int c = channel(g, j);
             const uint32_t first = ((uint32_t)origin + (uint32_t)c * m.HW) * (uint32_t)sizeof(T);  // modulo 2^32
-            return reinterpret_cast<R*>(s + c * geom.row + (first & 15) + pl * sizeof(T));
+            const T* p = reinterpret_cast<const T*>(s + c * geom.row + (first & 15)) + pl;
+#pragma unroll
+            for (int e = 0; e < VP; ++e) f[e] = e < live ? to_f(p[e * geom.lp]) : 0.0f;
         } else {
-            return reinterpret_cast<R*>(s) + (4 * g + j) * blockDim.x + threadIdx.x;
+            unpack(reinterpret_cast<const R*>(s)[(4 * g + j) * blockDim.x + threadIdx.x], f);
         }
     }
+    // To a map in global memory, rounded to its type.
+    __device__ __forceinline__ void store(void* to, int g, int j, const float (&f)[VP]) const {
+        T* p = static_cast<T*>(to) + origin + offset(g, j);
+        if constexpr (RAG) {
+#pragma unroll
+            for (int e = 0; e < VP; ++e)
+                if (e < live) p[e * geom.lp] = from_f<T>(f[e]);
+        } else {
+            *reinterpret_cast<R*>(p) = pack(f);
+        }
+    }
+    // r + dropout of f of quad g, into r.
+    __device__ __forceinline__ void drop(const MapDrop& d, uint32_t off, int g, const float (&f)[4][VP], float (&r)[4][VP]) const {
+        const int quad = channel(g, 0) / 4;
+        if (!RAG || d.mode != WTCONV_DROP_ELEMENT) {
+            drop_add_tile<VP>(d, off, row(), b, quad, f, r);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VP; ++e) {
+                const uint4 u = drop_words(d, off, row() + e * geom.lp, quad);
+                if (u.x >= d.thresh) r[0][e] = __fmaf_rn(f[0][e], d.grown, r[0][e]);
+                if (u.y >= d.thresh) r[1][e] = __fmaf_rn(f[1][e], d.grown, r[1][e]);
+                if (u.z >= d.thresh) r[2][e] = __fmaf_rn(f[2][e], d.grown, r[2][e]);
+                if (u.w >= d.thresh) r[3][e] = __fmaf_rn(f[3][e], d.grown, r[3][e]);
+            }
+        }
+    }
+
     // Starts the copy of tensor k of this tile; with skip, zeros.
     template <int G>
     __device__ __forceinline__ void fetch(int stage, int tensors, int k, const void* from, bool skip) const {
-        if constexpr (VP == 1) {
+        char* s = smem + (stage * tensors + k) * geom.tensor;
+        if constexpr (RAG) {
             const long long bytes = m.rows * m.C * (long long)sizeof(T);
-            const int pixels = min(geom.lp, m.HW - p0), chunks = geom.row / 16;
-            char* s = smem + (stage * tensors + k) * geom.tensor;
+            const int pixels = min(geom.lp * VP, m.HW - p0), chunks = geom.row / 16;
             const int n = m.C * chunks;
             for (int i = threadIdx.x; i < n; i += blockDim.x) {
                 const int c = (int)((__umulhi((uint32_t)i, geom.by_chunks.mul) + (uint32_t)i) >> geom.by_chunks.shift);
@@ -150,7 +186,7 @@ struct Tile {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const bool ok = in(g, j) && !skip;
-                    copy16(slot(stage, tensors, k, g, j), base + (ok ? offset(g, j) : 0u), ok ? 16 : 0);
+                    copy16(reinterpret_cast<R*>(s) + (4 * g + j) * blockDim.x + threadIdx.x, base + (ok ? offset(g, j) : 0u), ok ? 16 : 0);
                 }
             }
         }
@@ -159,22 +195,66 @@ struct Tile {
     // of them; their reads of the other stage are over).
     __device__ __forceinline__ void arrive() const {
         copies_wait<0>();
-        if constexpr (VP == 1) __syncthreads();
+        if constexpr (RAG) __syncthreads();
+    }
+};
+
+// One sum for each pixel of the tile over all owners of channels, through
+// `finish(pixel of the tile, sum)`, which runs once a pixel; every owner gets
+// its result.  smem: [warps + 1][lp * VP] floats.
+template <int VP, typename Tl, typename F>
+__device__ __forceinline__ void tile_sum(const Tl& tile, float (&v)[VP], float* smem, F finish) {
+    const int lp = tile.geom.lp, warps = blockDim.x / 32, lane = threadIdx.x % 32, px = lp * VP;
+    for (int o = lp; o < 32; o *= 2) {
+#pragma unroll
+        for (int e = 0; e < VP; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+    }
+    if (lane < lp) {
+#pragma unroll
+        for (int e = 0; e < VP; ++e) smem[(threadIdx.x / 32) * px + tile.pixel(e)] = v[e];
+    }
+    __syncthreads();
+    for (int p = threadIdx.x; p < px; p += blockDim.x) {
+        float s = smem[p];
+        for (int k = 1; k < warps; ++k) s += smem[k * px + p];
+        smem[warps * px + p] = finish(p, s);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VP; ++e) v[e] = smem[warps * px + tile.pixel(e)];
+}
+
+// h between the sum and the output: as stored, or as the floats that it stands for.
+template <typename T, int VP, bool RAG>
+struct Held {
+    typename Chunk<T, VP>::type v;
+    __device__ __forceinline__ void put(float (&f)[VP]) { v = pack(f), unpack(v, f); }
+    __device__ __forceinline__ void get(float (&f)[VP]) const { unpack(v, f); }
+};
+template <typename T, int VP>
+struct Held<T, VP, true> {
+    float v[VP];
+    __device__ __forceinline__ void put(float (&f)[VP]) {
+#pragma unroll
+        for (int e = 0; e < VP; ++e) v[e] = f[e] = to_f(from_f<T>(f[e]));
+    }
+    __device__ __forceinline__ void get(float (&f)[VP]) const {
+#pragma unroll
+        for (int e = 0; e < VP; ++e) f[e] = v[e];
     }
 };
 
 // G: quads of an owner (geom.iters), at compile time for what stays in registers.
-template <typename T, int VP, int G, int JOIN, bool Q8>
+template <typename T, int VP, bool RAG, int G, int JOIN, bool Q8>
 __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapShape m, NormFwdArgs a, MapDrop d, PlanesGeom geom) {
-    using R = typename Chunk<T, VP>::type;
     constexpr int NT = JOIN == kPlain ? 1 : 2;
     extern __shared__ __align__(16) char smem[];  // two stages; tile_sum's; (Q8) the groups' largest bits: [groups][px]
     float* sums = reinterpret_cast<float*>(smem + geom.head);
     const int px = geom.lp * VP, warps = blockDim.x / 32;
     const uint32_t offset = JOIN == kDropped ? drop_offset(d) : 0;
     const long long total = m.rows / m.HW * geom.tiles;
-    Tile<T, VP> now(m, geom, smem), next(m, geom, smem);
-    auto fetch = [&](const Tile<T, VP>& t, int stage) {
+    Tile<T, VP, RAG> now(m, geom, smem), next(m, geom, smem);
+    auto fetch = [&](const Tile<T, VP, RAG>& t, int stage) {
         bool skip = false;
         if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) skip = !keep_sample(d, offset, t.b);
         t.template fetch<G>(stage, NT, 0, a.x, skip);
@@ -194,55 +274,44 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
         now.at(tile);
         now.arrive();
         if (tile + gridDim.x < total) next.at(tile + gridDim.x), fetch(next, stage ^ 1);
-        R h[G][4];
+        Held<T, VP, RAG> h[G][4];
         float ss[VP] = {};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
+            float f[4][VP] = {};
             if (JOIN == kDropped) {
-                float f[4][VP] = {}, r[4][VP] = {};
+                float x[4][VP] = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (!now.in(g, j)) continue;
-                    unpack(*now.slot(stage, NT, 0, g, j), f[j]);
-                    unpack(*now.slot(stage, NT, 1, g, j), r[j]);
+                    now.load(stage, NT, 0, g, j, x[j]);
+                    now.load(stage, NT, 1, g, j, f[j]);
                 }
-                if (now.in(g, 0)) drop_add_tile<VP>(d, offset, now.row(), now.b, now.channel(g, 0) / 4, f, r);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    h[g][j] = Chunk<T, VP>::from(r[j]);
-                    if (now.in(g, j)) *now.chunk(a.h, g, j) = h[g][j];
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    h[g][j] = Chunk<T, VP>::zero();
-                    if (!now.in(g, j)) continue;
-                    h[g][j] = *now.slot(stage, NT, 0, g, j);
-                    if (JOIN == kResidual) {
-                        float f[VP], r[VP];
-                        unpack(h[g][j], f);
-                        unpack(*now.slot(stage, NT, 1, g, j), r);
-                        add_n(f, r);
-                        h[g][j] = Chunk<T, VP>::from(f);
-                        *now.chunk(a.h, g, j) = h[g][j];
-                    }
-                }
+                if (now.in(g, 0)) now.drop(d, offset, g, x, f);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float f[VP];
-                unpack(h[g][j], f);  // the norm is of h as it is stored
-                fma_n(f, f, ss);
+                if (JOIN != kDropped && now.in(g, j)) {
+                    now.load(stage, NT, 0, g, j, f[j]);
+                    if (JOIN == kResidual) {
+                        float r[VP];
+                        now.load(stage, NT, 1, g, j, r);
+                        add_n(f[j], r);
+                    }
+                }
+                h[g][j].put(f[j]);  // the norm is of h as it is stored
+                if (JOIN != kPlain && now.in(g, j)) now.store(a.h, g, j, f[j]);
+                fma_n(f[j], f[j], ss);
             }
         }
-        tile_sum<VP>(ss, geom.lp, sums, [&](int q, float s) {
+        tile_sum<VP>(now, ss, sums, [&](int q, float s) {
             const float r = rsqrtf(s / m.C + a.eps);
             if (a.rstd && now.p0 + q < m.HW) a.rstd[now.b * m.HW + now.p0 + q] = r;
             return r;
         });
         // v = h * r * w
         auto value = [&](int g, int j, float (&f)[VP]) {
-            unpack(h[g][j], f);
+            h[g][j].get(f);
             mul_n(f, ss);
             mul_n(f, w[g][j]);
         };
@@ -254,7 +323,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
                     if (!now.in(g, j)) continue;
                     float f[VP];
                     value(g, j, f);
-                    *now.chunk(a.y, g, j) = Chunk<T, VP>::from(f);
+                    now.store(a.y, g, j, f);
                 }
             }
         } else {
@@ -274,7 +343,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
                 }
                 if (now.in(g, 0)) {
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) atomicMax(&top[now.channel(g, 0) / a.group * px + now.pl * VP + e], bits[e]);
+                    for (int e = 0; e < VP; ++e)
+                        if (now.has(e)) atomicMax(&top[now.channel(g, 0) / a.group * px + now.pixel(e)], bits[e]);
                 }
             }
             __syncthreads();
@@ -290,14 +360,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
                 if (!now.in(g, 0)) continue;
                 float inv[VP];
 #pragma unroll
-                for (int e = 0; e < VP; ++e) inv[e] = __uint_as_float(top[now.channel(g, 0) / a.group * px + now.pl * VP + e]);
+                for (int e = 0; e < VP; ++e) inv[e] = __uint_as_float(top[now.channel(g, 0) / a.group * px + now.pixel(e)]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (!now.in(g, j)) continue;
                     float f[VP];
                     value(g, j, f);
                     mul_n(f, inv);
-                    q8_store<VP>(static_cast<uint8_t*>(a.y) + now.origin + now.offset(g, j), f, a.q8);
+                    uint8_t* q = static_cast<uint8_t*>(a.y) + now.origin + now.offset(g, j);
+                    if constexpr (RAG) {
+#pragma unroll
+                        for (int e = 0; e < VP; ++e)
+                            if (now.has(e)) q[e * geom.lp] = q8_one(f[e], a.q8);
+                    } else {
+                        q8_store<VP>(q, f, a.q8);
+                    }
                 }
             }
             __syncthreads();  // before the next tile clears `top`
@@ -305,17 +382,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
     }
 }
 
-template <typename T, int VP, int G, bool DROP>
+template <typename T, int VP, bool RAG, int G, bool DROP>
 __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(MapShape m, NormBwdArgs a, MapDrop d, PlanesGeom geom) {
-    using R = typename Chunk<T, VP>::type;
     extern __shared__ __align__(16) char smem[];
     float* sums = reinterpret_cast<float*>(smem + geom.head);
     const int NT = a.dh ? 3 : 2;
     const uint32_t offset = DROP ? drop_offset(d) : 0;
     const long long total = m.rows / m.HW * geom.tiles;
     const bool outputs = a.dres || (DROP && a.dx);
-    Tile<T, VP> now(m, geom, smem), next(m, geom, smem);
-    auto fetch = [&](const Tile<T, VP>& t, int stage) {
+    Tile<T, VP, RAG> now(m, geom, smem), next(m, geom, smem);
+    auto fetch = [&](const Tile<T, VP, RAG>& t, int stage) {
         t.template fetch<G>(stage, NT, 0, a.h, false);
         t.template fetch<G>(stage, NT, 1, a.dy, false);
         if (a.dh) t.template fetch<G>(stage, NT, 2, a.dh, false);
@@ -335,7 +411,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
         float r[VP] = {}, gh[VP] = {};
         if (now.live) {
 #pragma unroll
-            for (int e = 0; e < VP; ++e) r[e] = a.rstd[now.row() + e];
+            for (int e = 0; e < VP; ++e)
+                if (now.has(e)) r[e] = a.rstd[now.b * m.HW + now.p0 + now.pixel(e)];
         }
         now.arrive();
         if (tile + gridDim.x < total) next.at(tile + gridDim.x), fetch(next, stage ^ 1);
@@ -345,8 +422,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
             for (int j = 0; j < 4; ++j) {
                 if (!now.in(g, j)) continue;
                 float fh[VP], fg[VP], own[VP] = {};
-                unpack(*now.slot(stage, NT, 0, g, j), fh);
-                unpack(*now.slot(stage, NT, 1, g, j), fg);
+                now.load(stage, NT, 0, g, j, fh);
+                now.load(stage, NT, 1, g, j, fg);
                 mul_n(fg, fh);
                 fma_n(fg, w[g][j], gh);
                 fma_n(fg, r, own);
@@ -355,7 +432,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
             }
         }
         if (!outputs) continue;
-        tile_sum<VP>(gh, geom.lp, sums, [&](int, float s) { return s / m.C; });
+        tile_sum<VP>(now, gh, sums, [&](int, float s) { return s / m.C; });
         bool whole = true;
         if (DROP && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, now.b);
         // dres = dh + (r * w) * dy - (r^3 mean(g * h)) * h
@@ -368,25 +445,25 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
             for (int j = 0; j < 4; ++j) {
                 if (!now.in(g, j)) continue;
                 float fh[VP], fg[VP];
-                unpack(*now.slot(stage, NT, 0, g, j), fh);
-                unpack(*now.slot(stage, NT, 1, g, j), fg);
-                if (a.dh) unpack(*now.slot(stage, NT, 2, g, j), fe[j]);
+                now.load(stage, NT, 0, g, j, fh);
+                now.load(stage, NT, 1, g, j, fg);
+                if (a.dh) now.load(stage, NT, 2, g, j, fe[j]);
                 mul_n(fg, w[g][j]);
                 fma_n(fg, r, fe[j]);
                 fma_n(fh, gh, fe[j]);
-                if (a.dres) *now.chunk(a.dres, g, j) = Chunk<T, VP>::from(fe[j]);
+                if (a.dres) now.store(a.dres, g, j, fe[j]);
             }
             if (DROP && a.dx) {
                 float dx[4][VP] = {};
                 if (d.mode != WTCONV_DROP_SAMPLE) {
-                    if (now.in(g, 0)) drop_add_tile<VP>(d, offset, now.row(), now.b, now.channel(g, 0) / 4, fe, dx);
+                    if (now.in(g, 0)) now.drop(d, offset, g, fe, dx);
                 } else if (whole) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) fma_n(fe[j], d.grown, dx[j]);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (now.in(g, j)) *now.chunk(a.dx, g, j) = Chunk<T, VP>::from(dx[j]);
+                    if (now.in(g, j)) now.store(a.dx, g, j, dx[j]);
             }
         }
     }
@@ -416,29 +493,25 @@ int launch(K kernel, const MapShape& m, const A& a, const MapDrop& d, const Plan
     return (int)ctas;
 }
 
-template <typename T, int VP, int JOIN, bool Q8>
+template <typename T, int VP, bool RAG, int JOIN, bool Q8>
 bool run_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     PlanesGeom g;
-    if (!planes_geom(m, VP, sizeof(T), JOIN == kPlain ? 1 : 2, &g)) return false;
+    if (!planes_geom(m, VP, RAG, sizeof(T), JOIN == kPlain ? 1 : 2, &g)) return false;
     const int groups = Q8 ? (m.C + a.group - 1) / a.group : 0;
     const size_t smem = g.head + (size_t)(g.warps + 1 + groups) * g.lp * VP * 4;
     if (smem > 225 * 1024) return false;
-    switch (g.iters) {
-        case 1: launch(wtconv_norm_planes_kernel<T, VP, 1, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s); break;
-        case 2: launch(wtconv_norm_planes_kernel<T, VP, 2, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s); break;
-        default:
-            if constexpr (VP == 1) launch(wtconv_norm_planes_kernel<T, VP, 4, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
-    }
+    if (g.iters == 1) launch(wtconv_norm_planes_kernel<T, VP, RAG, 1, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
+    else launch(wtconv_norm_planes_kernel<T, VP, RAG, 2, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
     return true;
 }
 
-template <typename T, int VP>
+template <typename T, int VP, bool RAG>
 bool pick_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     if (a.q8 >= 0)
-        return a.residual ? run_fwd<T, VP, kResidual, true>(m, a, d, sms, s) : run_fwd<T, VP, kPlain, true>(m, a, d, sms, s);
-    if (!a.residual) return run_fwd<T, VP, kPlain, false>(m, a, d, sms, s);
-    if (!d.on) return run_fwd<T, VP, kResidual, false>(m, a, d, sms, s);
-    return run_fwd<T, VP, kDropped, false>(m, a, d, sms, s);
+        return a.residual ? run_fwd<T, VP, RAG, kResidual, true>(m, a, d, sms, s) : run_fwd<T, VP, RAG, kPlain, true>(m, a, d, sms, s);
+    if (!a.residual) return run_fwd<T, VP, RAG, kPlain, false>(m, a, d, sms, s);
+    if (!d.on) return run_fwd<T, VP, RAG, kResidual, false>(m, a, d, sms, s);
+    return run_fwd<T, VP, RAG, kDropped, false>(m, a, d, sms, s);
 }
 
 bool aligned(std::initializer_list<const void*> ps) {
@@ -451,23 +524,18 @@ template <typename T>
 bool fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     constexpr int V = kVec<T>;
     if (!aligned({a.x, a.residual})) return false;
-    if (m.HW % V == 0 && aligned({a.h}) && (uintptr_t)a.y % (a.q8 >= 0 ? V : 16) == 0) return pick_fwd<T, V>(m, a, d, sms, s);
-    return pick_fwd<T, 1>(m, a, d, sms, s);
+    if (m.HW % V == 0 && aligned({a.h}) && (uintptr_t)a.y % (a.q8 >= 0 ? V : 16) == 0) return pick_fwd<T, V, false>(m, a, d, sms, s);
+    return pick_fwd<T, kRagged, true>(m, a, d, sms, s);
 }
 
-template <typename T, int VP, bool DROP>
+template <typename T, int VP, bool RAG, bool DROP>
 int run_bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     PlanesGeom g;
-    if (!planes_geom(m, VP, sizeof(T), a.dh ? 3 : 2, &g)) return 0;
+    if (!planes_geom(m, VP, RAG, sizeof(T), a.dh ? 3 : 2, &g)) return 0;
     const size_t smem = g.head + (size_t)(g.warps + 1) * g.lp * VP * 4;
     const long long most = norm_parts(m, sms);
-    switch (g.iters) {
-        case 1: return launch(wtconv_norm_planes_bwd_kernel<T, VP, 1, DROP>, m, a, d, g, smem, most, sms, s);
-        case 2: return launch(wtconv_norm_planes_bwd_kernel<T, VP, 2, DROP>, m, a, d, g, smem, most, sms, s);
-        default:
-            if constexpr (VP == 1) return launch(wtconv_norm_planes_bwd_kernel<T, VP, 4, DROP>, m, a, d, g, smem, most, sms, s);
-    }
-    return 0;
+    return g.iters == 1 ? launch(wtconv_norm_planes_bwd_kernel<T, VP, RAG, 1, DROP>, m, a, d, g, smem, most, sms, s)
+                        : launch(wtconv_norm_planes_bwd_kernel<T, VP, RAG, 2, DROP>, m, a, d, g, smem, most, sms, s);
 }
 
 // The number of partial vectors, or 0 if the map is not one for these kernels.
@@ -476,8 +544,8 @@ int bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cuda
     constexpr int V = kVec<T>;
     if (!aligned({a.h, a.dy, a.dh})) return 0;
     if (m.HW % V == 0 && aligned({a.dres, a.dx}))
-        return a.dx ? run_bwd<T, V, true>(m, a, d, sms, s) : run_bwd<T, V, false>(m, a, d, sms, s);
-    return a.dx ? run_bwd<T, 1, true>(m, a, d, sms, s) : run_bwd<T, 1, false>(m, a, d, sms, s);
+        return a.dx ? run_bwd<T, V, false, true>(m, a, d, sms, s) : run_bwd<T, V, false, false>(m, a, d, sms, s);
+    return a.dx ? run_bwd<T, kRagged, true, true>(m, a, d, sms, s) : run_bwd<T, kRagged, true, false>(m, a, d, sms, s);
 }
 
 }  // namespace

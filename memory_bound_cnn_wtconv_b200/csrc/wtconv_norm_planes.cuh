@@ -28,7 +28,7 @@ __device__ __forceinline__ uint32_t keep_tile(const MapDrop& d, uint32_t offset,
 // `finish(pixel of the tile, sum)`, which runs once a pixel; every owner gets
 // its result.  smem: [warps + 1][lp * VP] floats.
 template <int VP, typename F>
-__device__ __forceinline__ void tile_sum(float (&v)[VP], int lp, float* smem, F finish) {
+__device__ __forceinline__ void lane_tile_sum(float (&v)[VP], int lp, float* smem, F finish) {
     const int warps = blockDim.x / 32, lane = threadIdx.x % 32, pl = lane & (lp - 1), px = lp * VP;
     for (int o = lp; o < 32; o *= 2) {
 #pragma unroll
@@ -53,7 +53,7 @@ __device__ __forceinline__ void tile_sum(float (&v)[VP], int lp, float* smem, F 
 template <int VP>
 __device__ __forceinline__ void q8_store(uint8_t* o, const float (&f)[VP], int q8) {
     if constexpr (VP == 1) {
-        *o = (uint8_t)q8_pack4(f[0], 0.0f, 0.0f, 0.0f, q8);
+        *o = q8_one(f[0], q8);
     } else if constexpr (VP == 4) {
         *reinterpret_cast<uint32_t*>(o) = q8_pack4(f[0], f[1], f[2], f[3], q8);
     } else {

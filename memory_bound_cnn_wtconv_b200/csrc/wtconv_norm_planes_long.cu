@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_kernel(Ma
                 ss[0] += f * f;
             }
         }
-        tile_sum<1>(ss, lp, smem, [&](int q, float s) {
+        lane_tile_sum<1>(ss, lp, smem, [&](int q, float s) {
             const float r = rsqrtf(s / m.C + a.eps);
             if (a.rstd && p0 + q < m.HW) a.rstd[b * m.HW + p0 + q] = r;
             return r;
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_bwd_kerne
                 if (live && c < m.C) gh[0] += to_f(dy[(long long)c * m.HW]) * to_f(h[(long long)c * m.HW]) * a.weight[c];
             }
         }
-        tile_sum<1>(gh, lp, smem, [&](int, float s) { return s / m.C; });
+        lane_tile_sum<1>(gh, lp, smem, [&](int, float s) { return s / m.C; });
         const float s = gh[0] * r * r;
         for (int g = 0; g < iters; ++g) {
             const int quad = g * owners + owner;

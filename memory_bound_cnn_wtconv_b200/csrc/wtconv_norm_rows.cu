@@ -24,6 +24,8 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
             if (i * tpr + t < slots) load_weight<V>(a.weight + (i * tpr + t) * V, w[i]);
         }
     }
+    long long decided = -1;  // the last sample that a decision was drawn for
+    bool kept = true;
     // Every thread of a CTA makes the same number of rounds.
     for (long long row0 = (long long)blockIdx.x * step; row0 < m.rows; row0 += (long long)gridDim.x * step) {
         const long long row = row0 + threadIdx.x / tpr;
@@ -35,8 +37,11 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
         long long drow = 0;
         bool whole = true;  // a sample's decision
         if (JOIN == kDropped) {
-            drow = drop_row(d, m, row);
-            if (d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, drow);
+            drow = drop_row(d, row);
+            if (d.mode == WTCONV_DROP_SAMPLE) {  // neighbouring rows are mostly of one sample
+                if (drow != decided) kept = keep_sample(d, offset, drow), decided = drow;
+                whole = kept;
+            }
         }
         auto in = [&](int i) { return live && i * tpr + t < slots; };
         R raw[NR];
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
                     mul_n(f, 1.0f / scale);  // one rounding more than v / scale
                     uint8_t* q = static_cast<uint8_t*>(a.y) + base + c;
                     if constexpr (V == 1) {
-                        *q = (uint8_t)q8_pack4(f[0], 0.0f, 0.0f, 0.0f, a.q8);
+                        *q = q8_one(f[0], a.q8);
                     } else if constexpr (V == 4) {
                         *reinterpret_cast<uint32_t*>(q) = q8_pack4(f[0], f[1], f[2], f[3], a.q8);
                     } else {

@@ -25,6 +25,8 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
             if (i * tpr + t < slots) load_weight<V>(a.weight + (i * tpr + t) * V, w[i]);
         }
     }
+    long long decided = -1;
+    bool kept = true;
     for (long long row0 = (long long)blockIdx.x * step; row0 < m.rows; row0 += (long long)gridDim.x * step) {
         const long long row = row0 + threadIdx.x / tpr;
         const bool live = row < m.rows;
@@ -36,8 +38,11 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
         long long drow = 0;
         bool whole = true;
         if (DROP) {
-            drow = drop_row(d, m, row);
-            if (d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, drow);
+            drow = drop_row(d, row);
+            if (d.mode == WTCONV_DROP_SAMPLE) {  // neighbouring rows are mostly of one sample
+                if (drow != decided) kept = keep_sample(d, offset, drow), decided = drow;
+                whole = kept;
+            }
         }
         auto in = [&](int i) { return live && i * tpr + t < slots; };
         R hr[NR], gr[NR], er[NR];
