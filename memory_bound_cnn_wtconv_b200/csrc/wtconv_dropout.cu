@@ -85,19 +85,21 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_planes_kernel(MapShap
         for (int j = 0; j < 4; ++j) {
             const bool in = 4 * quad + j < m.C;
             rx[j] = in ? *reinterpret_cast<const R*>(x + (long long)j * m.HW) : Chunk<T, VP>::zero();
-            if (RES) rr[j] = in ? *reinterpret_cast<const R*>(res + (long long)j * m.HW) : Chunk<T, VP>::zero();
+            rr[j] = RES && in ? *reinterpret_cast<const R*>(res + (long long)j * m.HW) : Chunk<T, VP>::zero();
         }
-        float f[4][VP], r[4][VP] = {};
+        if constexpr (VP > 1) {
+            drop_add_chunks<T>(d, offset, b * m.HW + p, b, quad, rx, rr);
+        } else {
+            float f[4][1], r[4][1];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            unpack(rx[j], f[j]);
-            if (RES) unpack(rr[j], r[j]);
+            for (int j = 0; j < 4; ++j) unpack(rx[j], f[j]), unpack(rr[j], r[j]);
+            drop_add_tile<1>(d, offset, b * m.HW + p, b, quad, f, r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) rr[j] = from_f<T>(r[j][0]);
         }
-        drop_add_tile<VP>(d, offset, b * m.HW + p, b, quad, f, r);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (4 * quad + j < m.C)
-                *reinterpret_cast<R*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = Chunk<T, VP>::from(r[j]);
+            if (4 * quad + j < m.C) *reinterpret_cast<R*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = rr[j];
     }
 }
 

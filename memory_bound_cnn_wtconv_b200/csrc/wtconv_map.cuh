@@ -156,6 +156,48 @@ __device__ __forceinline__ void drop_add4(const MapDrop& d, const uint4& u, cons
     if (u.z >= d.thresh) r[2] = __fmaf_rn(f[2], d.grown, r[2]);
     if (u.w >= d.thresh) r[3] = __fmaf_rn(f[3], d.grown, r[3]);
 }
+// T(r + d * x) of a 16-byte chunk of pixels of four channels, into r, chunk word
+// by chunk word, so that few values are held as floats at once.
+template <typename T>
+__device__ __forceinline__ void drop_add_words(const MapDrop& d, const uint4 (&u)[sizeof(uint32_t) / sizeof(T)], uint32_t x, uint32_t& r, int j) {
+    auto word = [&](int v) { return j == 0 ? u[v].x : j == 1 ? u[v].y : j == 2 ? u[v].z : u[v].w; };
+    if constexpr (sizeof(T) == 4) {
+        if (word(0) >= d.thresh) r = __float_as_uint(__fmaf_rn(__uint_as_float(x), d.grown, __uint_as_float(r)));
+    } else {
+        float lo = __uint_as_float(r << 16), hi = __uint_as_float(r & 0xffff0000u);
+        if (word(0) >= d.thresh) lo = __fmaf_rn(__uint_as_float(x << 16), d.grown, lo);
+        if (word(1) >= d.thresh) hi = __fmaf_rn(__uint_as_float(x & 0xffff0000u), d.grown, hi);
+        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        r = *reinterpret_cast<const uint32_t*>(&p);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void drop_add_chunks(const MapDrop& d, uint32_t offset, long long row, long long b, int quad,
+                                                const uint4 (&x)[4], uint4 (&r)[4]) {
+    constexpr int N = sizeof(uint32_t) / sizeof(T);  // pixels of a word
+    const uint32_t lo = (uint32_t)row, hi = (uint32_t)((unsigned long long)row >> 32);
+    uint4 u[N];
+    const bool element = d.mode == WTCONV_DROP_ELEMENT;
+    if (!element) {
+        u[0] = drop_words(d, offset, b, d.mode == WTCONV_DROP_SAMPLE ? 0 : quad);
+        if (d.mode == WTCONV_DROP_SAMPLE) u[0].y = u[0].z = u[0].w = u[0].x;
+        u[N - 1] = u[0];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (element) {
+#pragma unroll
+            for (int v = 0; v < N; ++v) u[v] = drop_words(d, offset, lo + k * N + v, hi, quad);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t xk = k == 0 ? x[j].x : k == 1 ? x[j].y : k == 2 ? x[j].z : x[j].w;
+            uint32_t& rk = k == 0 ? r[j].x : k == 1 ? r[j].y : k == 2 ? r[j].z : r[j].w;
+            drop_add_words<T>(d, u, xk, rk, j);
+        }
+    }
+}
+
 // r + d * f of N pixels of four channels, into r; lo: the first pixel's row,
 // a multiple of N; b: the sample.
 template <int N>

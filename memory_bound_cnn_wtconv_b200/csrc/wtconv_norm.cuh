@@ -25,11 +25,18 @@ int norm_resident(K kernel, int threads, size_t smem) {
 // How JOIN reads h: x itself, residual + x, or residual + dropout of x.
 enum { kPlain = 0, kResidual = 1, kDropped = 2 };
 
-// The scale of a group whose largest |v| has these bits, and its inverse's
-// place: q = v / scale.
+// The scale of a group whose largest |v| has these bits (one rounding more than
+// the quotient), and what its values are multiplied with: the reciprocal to one
+// unit in the last place, so that q is v / scale with two roundings more, far
+// within its own rounding to 8 bits.
 __device__ __forceinline__ float q8_scale(uint32_t bits, int q8) {
-    const float s = __uint_as_float(bits) / (q8 == WTCONV_E4M3 ? 448.0f : 127.0f);
+    const float s = __uint_as_float(bits) * (q8 == WTCONV_E4M3 ? 1.0f / 448.0f : 1.0f / 127.0f);
     return s < 1.17549435e-38f ? 1.17549435e-38f : s;  // a NaN stays
+}
+__device__ __forceinline__ float q8_inverse(float scale) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(scale));
+    return r;
 }
 
 // Four values to four bytes.

@@ -114,6 +114,19 @@ struct Tile {
         const int left = m.HW - p0 - pixel(0);  // chunks: HW is a multiple of VP
         live = !RAG ? (left > 0 ? VP : 0) : left <= 0 ? 0 : min(VP, (left - 1) / geom.lp + 1);
     }
+    // This thread's pixels of one value for each of the tile's.
+    __device__ __forceinline__ void get(const float* p, float (&v)[VP]) const {
+        if constexpr (RAG) {
+#pragma unroll
+            for (int e = 0; e < VP; ++e) v[e] = p[pixel(e)];
+        } else {
+#pragma unroll
+            for (int e = 0; e < VP; e += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(p + pixel(e));
+                v[e] = q.x, v[e + 1] = q.y, v[e + 2] = q.z, v[e + 3] = q.w;
+            }
+        }
+    }
     __device__ __forceinline__ bool has(int e) const { return RAG ? e < live : true; }
     __device__ __forceinline__ long long row() const { return b * m.HW + p0 + pixel(0); }
     __device__ __forceinline__ int channel(int g, int j) const { return 4 * (g * geom.owners + owner) + j; }
@@ -121,17 +134,20 @@ struct Tile {
     // This thread's first pixel of channel(g, j), from the tile's first element on.
     __device__ __forceinline__ uint32_t offset(int g, int j) const { return own + (uint32_t)(4 * g * geom.owners + j) * m.HW; }
 
+    __device__ __forceinline__ uint4 raw(int stage, int tensors, int k, int g, int j) const {
+        return reinterpret_cast<const uint4*>(smem + (stage * tensors + k) * geom.tensor)[(4 * g + j) * blockDim.x + threadIdx.x];
+    }
     // This thread's pixels of channel(g, j) of tensor k of a stage, as floats.
     __device__ __forceinline__ void load(int stage, int tensors, int k, int g, int j, float (&f)[VP]) const {
-        const char* s = smem + (stage * tensors + k) * geom.tensor;
         if constexpr (RAG) {
+            const char* s = smem + (stage * tensors + k) * geom.tensor;
             const int c = channel(g, j);
             const uint32_t first = ((uint32_t)origin + (uint32_t)c * m.HW) * (uint32_t)sizeof(T);  // modulo 2^32
             const T* p = reinterpret_cast<const T*>(s + c * geom.row + (first & 15)) + pl;
 #pragma unroll
             for (int e = 0; e < VP; ++e) f[e] = e < live ? to_f(p[e * geom.lp]) : 0.0f;
         } else {
-            unpack(reinterpret_cast<const R*>(s)[(4 * g + j) * blockDim.x + threadIdx.x], f);
+            unpack(raw(stage, tensors, k, g, j), f);
         }
     }
     // To a map in global memory, rounded to its type.
@@ -220,8 +236,7 @@ __device__ __forceinline__ void tile_sum(const Tl& tile, float (&v)[VP], float* 
         smem[warps * px + p] = finish(p, s);
     }
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < VP; ++e) v[e] = smem[warps * px + tile.pixel(e)];
+    tile.get(smem + warps * px, v);
 }
 
 // h between the sum and the output: as stored, or as the floats that it stands for.
@@ -279,7 +294,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float f[4][VP] = {};
-            if (JOIN == kDropped) {
+            if constexpr (JOIN == kDropped && !RAG) {
+                uint4 x[4] = {}, r[4] = {};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!now.in(g, j)) continue;
+                    x[j] = now.raw(stage, NT, 0, g, j);
+                    r[j] = now.raw(stage, NT, 1, g, j);
+                }
+                if (now.in(g, 0)) drop_add_chunks<T>(d, offset, now.row(), now.b, now.channel(g, 0) / 4, x, r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) unpack(r[j], f[j]);
+            } else if (JOIN == kDropped) {
                 float x[4][VP] = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -341,7 +367,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
 #pragma unroll
                     for (int e = 0; e < VP; ++e) bits[e] = max(bits[e], abs_bits(f[e]));
                 }
-                if (now.in(g, 0)) {
+                // The lanes of a group first, then one of them to shared memory.
+                int o = geom.lp;
+                for (; o < 32 && o / geom.lp * 4 < a.group; o *= 2) {
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) bits[e] = max(bits[e], __shfl_xor_sync(0xffffffffu, bits[e], o));
+                }
+                if (now.in(g, 0) && (threadIdx.x & (o - 1) & ~(geom.lp - 1)) == 0) {
 #pragma unroll
                     for (int e = 0; e < VP; ++e)
                         if (now.has(e)) atomicMax(&top[now.channel(g, 0) / a.group * px + now.pixel(e)], bits[e]);
@@ -350,7 +382,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
             __syncthreads();
             for (int q = threadIdx.x; q < groups * px; q += blockDim.x) {
                 const float s = q8_scale(top[q], a.q8);
-                top[q] = __float_as_uint(1.0f / s);  // one rounding more than v / scale
+                top[q] = __float_as_uint(q8_inverse(s));
                 const int gr = q / px, pixel = now.p0 + q - gr * px;
                 if (pixel < m.HW) a.scale[(now.b * groups + gr) * m.HW + pixel] = s;
             }
@@ -359,8 +391,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
             for (int g = 0; g < G; ++g) {
                 if (!now.in(g, 0)) continue;
                 float inv[VP];
-#pragma unroll
-                for (int e = 0; e < VP; ++e) inv[e] = __uint_as_float(top[now.channel(g, 0) / a.group * px + now.pixel(e)]);
+                now.get(reinterpret_cast<const float*>(top) + now.channel(g, 0) / a.group * px, inv);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (!now.in(g, j)) continue;

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_kernel(Ma
             __syncthreads();
             for (int q = threadIdx.x; q < n * lp; q += blockDim.x) {
                 const float s = q8_scale(top[q], a.q8);
-                top[q] = __float_as_uint(1.0f / s);  // one rounding more than v / scale
+                top[q] = __float_as_uint(q8_inverse(s));
                 const int gr = first + q / lp, pixel = p0 + q % lp;
                 if (gr < groups && pixel < m.HW) a.scale[(b * groups + gr) * m.HW + pixel] = s;
             }

@@ -128,32 +128,38 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
             }
         } else {
             const int groups = (m.C + a.group - 1) / a.group;
-            auto largest = [&](int i0, int i) {
-                float f[V];
-                value(i0, i, f);
+            float v[NR][V];
+            auto values = [&](int i0) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i) value(i0, i, v[i]);
+            };
+            auto largest = [&](int i) {
                 uint32_t bits = 0;
 #pragma unroll
-                for (int e = 0; e < V; ++e) bits = max(bits, abs_bits(f[e]));
+                for (int e = 0; e < V; ++e) bits = max(bits, abs_bits(v[i][e]));
                 return bits;
             };
             float scale = 0.0f;
+            if (NV) values(0);
             if (groups == 1) {
                 uint32_t bits = 0;
                 for (int i0 = 0; i0 < iters; i0 += NR) {
+                    if (!NV) values(i0);
 #pragma unroll
-                    for (int i = 0; i < NR; ++i) bits = max(bits, largest(i0, i));
+                    for (int i = 0; i < NR; ++i) bits = max(bits, largest(i));
                 }
                 scale = q8_scale(team_max(bits, tpr, red), a.q8);
                 if (live && t == 0) a.scale[row] = scale;
             }
             auto out = [&](int i0) {
+                if (!NV) values(i0);
                 uint32_t bits[NR];
                 if (groups > 1) {
                     // A group is group / V neighbouring slots of a round, a power of two of neighbouring lanes; of single
                     // channels (teams of one warp) up to four whole rounds.
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
-                        bits[i] = largest(i0, i);
+                        bits[i] = largest(i);
                         for (int o = min(a.group / V, 32) / 2; o; o >>= 1) bits[i] = max(bits[i], __shfl_xor_sync(0xffffffffu, bits[i], o));
                     }
                     if constexpr (V == 1) {
@@ -173,12 +179,11 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
                     const int c = ((i0 + i) * tpr + t) * V;
                     if (groups > 1) {
                         scale = q8_scale(bits[i], a.q8);
-                        if (in(i0 + i) && c % a.group == 0) a.scale[row * groups + c / a.group] = scale;
+                        if (in(i0 + i) && (c & (a.group - 1)) == 0) a.scale[row * groups + c / a.group] = scale;
                     }
-                    float f[V];
-                    value(i0, i, f);
                     if (!in(i0 + i)) continue;
-                    mul_n(f, 1.0f / scale);  // one rounding more than v / scale
+                    float (&f)[V] = v[i];
+                    mul_n(f, q8_inverse(scale));
                     uint8_t* q = static_cast<uint8_t*>(a.y) + base + c;
                     if constexpr (V == 1) {
                         *q = q8_one(f[0], a.q8);
