@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kMaxWarps = 16;
 constexpr int kSmem = 200 * 1024;      // of the 227 KB a CTA may have
-constexpr int kSmemTwo = 110 * 1024;   // two CTAs an SM
+constexpr int kSmemTwo = 104 * 1024;   // two CTAs an SM, with their sums
 
 constexpr int kRagged = 4;  // pixels of a thread where planes are ragged
 
@@ -40,6 +40,7 @@ struct PlanesGeom {
     int head;                      // bytes of both stages
     FastDiv by_chunks;             // ragged: row / 16
     Divide by_tiles;
+    float per_channel;             // 1 / C
 };
 
 // Tiles of 128 bytes of a plane (256 where it is ragged, so that the chunks at
@@ -65,11 +66,12 @@ bool planes_geom(const MapShape& m, int VP, bool ragged, int esize, int tensors,
         g.row = (lp * VP * esize + 15) / 16 * 16 + 16;
         const long long tensor = ragged ? (long long)g.row * m.C : 64LL * g.iters * g.warps * 32;
         if (2 * tensors * tensor > kSmem) continue;
-        if (2 * tensors * tensor > kSmemTwo && lp * VP * esize > 64) continue;
+        if (2 * tensors * tensor + (g.warps + 1) * lp * VP * 4 > kSmemTwo && lp * VP * esize > 64) continue;
         g.tensor = (int)tensor;
         g.head = (int)(2 * tensors * tensor);
         g.by_chunks = make_fastdiv(g.row / 16);
         g.by_tiles = divide_by(g.tiles, m.rows);
+        g.per_channel = 1.0f / m.C;
         *out = g;
         return true;
     }
@@ -178,10 +180,10 @@ struct Tile {
         }
     }
 
-    // Starts the copy of tensor k of this tile; with skip, zeros.
-    template <int G>
-    __device__ __forceinline__ void fetch(int stage, int tensors, int k, const void* from, bool skip) const {
-        char* s = smem + (stage * tensors + k) * geom.tensor;
+    // Starts the copies of this tile's tensors; with skip, zeros for the first.
+    template <int G, int NT>
+    __device__ __forceinline__ void fetch(int stage, const void* const (&from)[NT], int tensors, bool skip) const {
+        char* s = smem + stage * tensors * geom.tensor;
         if constexpr (RAG) {
             const long long bytes = m.rows * m.C * (long long)sizeof(T);
             const int pixels = min(geom.lp * VP, m.HW - p0), chunks = geom.row / 16;
@@ -193,16 +195,23 @@ struct Tile {
                 const int span = (int)(first & 15) + pixels * (int)sizeof(T);  // from the chunk boundary on
                 if (16 * q >= span) continue;
                 const long long at = (first & ~15LL) + 16 * q;
-                copy16(s + c * geom.row + 16 * q, static_cast<const char*>(from) + at, skip ? 0 : (int)min(16LL, bytes - at));
+                const int count = (int)min(16LL, bytes - at);
+                char* to = s + c * geom.row + 16 * q;
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+                    if (k < tensors) copy16(to + k * geom.tensor, static_cast<const char*>(from[k]) + at, k == 0 && skip ? 0 : count);
             }
         } else {
-            const T* base = static_cast<const T*>(from) + origin;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const bool ok = in(g, j) && !skip;
-                    copy16(reinterpret_cast<R*>(s) + (4 * g + j) * blockDim.x + threadIdx.x, base + (ok ? offset(g, j) : 0u), ok ? 16 : 0);
+                    const bool ok = in(g, j);
+                    const long long at = origin + (ok ? offset(g, j) : 0u);
+                    char* to = s + ((4 * g + j) * blockDim.x + threadIdx.x) * 16;
+#pragma unroll
+                    for (int k = 0; k < NT; ++k)
+                        if (k < tensors) copy16(to + k * geom.tensor, static_cast<const T*>(from[k]) + at, ok && !(k == 0 && skip) ? 16 : 0);
                 }
             }
         }
@@ -272,8 +281,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
     auto fetch = [&](const Tile<T, VP, RAG>& t, int stage) {
         bool skip = false;
         if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) skip = !keep_sample(d, offset, t.b);
-        t.template fetch<G>(stage, NT, 0, a.x, skip);
-        if (JOIN != kPlain) t.template fetch<G>(stage, NT, 1, a.residual, false);
+        const void* const from[2] = {a.x, a.residual};
+        t.template fetch<G>(stage, from, NT, skip);
         copies_commit();
     };
     float w[G][4];
@@ -298,11 +307,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
                 uint4 x[4] = {}, r[4] = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (!now.in(g, j)) continue;
-                    x[j] = now.raw(stage, NT, 0, g, j);
+                    x[j] = now.raw(stage, NT, 0, g, j);  // zeros past the map's end
                     r[j] = now.raw(stage, NT, 1, g, j);
                 }
-                if (now.in(g, 0)) drop_add_chunks<T>(d, offset, now.row(), now.b, now.channel(g, 0) / 4, x, r);
+                drop_add_chunks<T>(d, offset, now.row(), now.b, now.channel(g, 0) / 4, x, r);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) unpack(r[j], f[j]);
             } else if (JOIN == kDropped) {
@@ -317,7 +325,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (JOIN != kDropped && now.in(g, j)) {
+                if (JOIN != kDropped && (!RAG || now.in(g, j))) {  // chunks: zeros past the map's end
                     now.load(stage, NT, 0, g, j, f[j]);
                     if (JOIN == kResidual) {
                         float r[VP];
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
             }
         }
         tile_sum<VP>(now, ss, sums, [&](int q, float s) {
-            const float r = rsqrtf(s / m.C + a.eps);
+            const float r = rsqrtf(s * geom.per_channel + a.eps);
             if (a.rstd && now.p0 + q < m.HW) a.rstd[now.b * m.HW + now.p0 + q] = r;
             return r;
         });
@@ -346,10 +354,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
             for (int g = 0; g < G; ++g) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (!now.in(g, j)) continue;
                     float f[VP];
                     value(g, j, f);
-                    now.store(a.y, g, j, f);
+                    if (now.in(g, j)) now.store(a.y, g, j, f);
                 }
             }
         } else {
@@ -423,9 +430,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
     const bool outputs = a.dres || (DROP && a.dx);
     Tile<T, VP, RAG> now(m, geom, smem), next(m, geom, smem);
     auto fetch = [&](const Tile<T, VP, RAG>& t, int stage) {
-        t.template fetch<G>(stage, NT, 0, a.h, false);
-        t.template fetch<G>(stage, NT, 1, a.dy, false);
-        if (a.dh) t.template fetch<G>(stage, NT, 2, a.dh, false);
+        const void* const from[3] = {a.h, a.dy, a.dh};
+        t.template fetch<G>(stage, from, NT, false);
         copies_commit();
     };
     float w[G][4], acc[G][4] = {};
@@ -451,7 +457,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
         for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (!now.in(g, j)) continue;
+                if (RAG && !now.in(g, j)) continue;  // chunks: zeros past the map's end
                 float fh[VP], fg[VP], own[VP] = {};
                 now.load(stage, NT, 0, g, j, fh);
                 now.load(stage, NT, 1, g, j, fg);
@@ -463,7 +469,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
             }
         }
         if (!outputs) continue;
-        tile_sum<VP>(now, gh, sums, [&](int, float s) { return s / m.C; });
+        tile_sum<VP>(now, gh, sums, [&](int, float s) { return s * geom.per_channel; });
         bool whole = true;
         if (DROP && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, now.b);
         // dres = dh + (r * w) * dy - (r^3 mean(g * h)) * h
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
             float fe[4][VP] = {};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (!now.in(g, j)) continue;
+                if (RAG && !now.in(g, j)) continue;
                 float fh[VP], fg[VP];
                 now.load(stage, NT, 0, g, j, fh);
                 now.load(stage, NT, 1, g, j, fg);
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
                 mul_n(fg, w[g][j]);
                 fma_n(fg, r, fe[j]);
                 fma_n(fh, gh, fe[j]);
-                if (a.dres) now.store(a.dres, g, j, fe[j]);
+                if (a.dres && now.in(g, j)) now.store(a.dres, g, j, fe[j]);
             }
             if (DROP && a.dx) {
                 float dx[4][VP] = {};

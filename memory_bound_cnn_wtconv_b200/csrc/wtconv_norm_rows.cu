@@ -8,8 +8,9 @@ namespace wtc {
 
 namespace {
 
-template <typename T, int V, int NV, int JOIN, bool Q8>
-__global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, NormFwdArgs a, MapDrop d, int tpr) {
+template <typename T, int V, int NV, int TPR, int JOIN, bool Q8>
+__global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, NormFwdArgs a, MapDrop d, int team, float per_channel) {
+    const int tpr = TPR ? TPR : team;
     using R = typename Chunk<T, V>::type;
     // Slots at once: all of them, or for NV = 0 one (four, where quads are exchanged).
     constexpr int NR = NV ? NV : V == 1 ? 4 : 1;
@@ -17,7 +18,7 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
     const int t = threadIdx.x % tpr, step = blockDim.x / tpr, slots = (m.C + V - 1) / V;
     const int iters = NV ? NV : (slots + tpr - 1) / tpr;
     const uint32_t offset = JOIN == kDropped ? drop_offset(d) : 0;
-    float w[NR][V];  // the weights of this thread's channels, for all its rows
+    float w[NR][V] = {};  // the weights of this thread's channels, for all its rows
     if (NV) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
@@ -94,12 +95,12 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
             for (int i0 = 0; i0 < iters; i0 += NR) join(i0);
         }
         ss = team_sum(ss, tpr, red);
-        const float r = rsqrtf(ss / m.C + a.eps);
+        const float r = rsqrtf(ss * per_channel + a.eps);
         if (a.rstd && live && t == 0) a.rstd[row] = r;
         // v = h * r * w of slot i0 + i (0 past the row's end)
         auto value = [&](int i0, int i, float (&f)[V]) {
             const int c = ((i0 + i) * tpr + t) * V;
-            if (!in(i0 + i)) {
+            if (!NV && !in(i0 + i)) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) f[e] = 0.0f;
                 return;
@@ -206,36 +207,16 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
 
 template <typename T, int V, int JOIN, bool Q8>
 void run(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
-    RowsGeom g;
-    if (V == 1 && Q8 && a.group < m.C) {
-        // Groups of single channels: a warp to a row, so that a group is whole rounds of it or a part of one.
-        const int nv = rows_nv(m.C, 32, 1);
-        g = RowsGeom{32, nv, kTeamThreads, kTeamThreads / 32};
-    } else {
-        // At least four threads (64 adjacent bytes, a quad's lanes); with groups, what makes a round whole groups.
-        g = rows_geom(m, V, Q8 && a.group < m.C ? std::max(4, a.group / V) : 4, sms);
-    }
+    // With groups, what makes a round of slots whole groups (single channels: a warp, to which a group is whole rounds
+    // or a part of one).
+    const bool grouped = Q8 && a.group < m.C;
+    const RowsGeom g = rows_geom(m, V, !grouped ? 0 : V == 1 ? 32 : a.group / V, grouped && V == 1, sms);
     const long long ctas = (m.rows + g.step - 1) / g.step;
     auto go = [&](auto kernel) {
         const unsigned grid = (unsigned)std::min(ctas, ctas <= 2LL * sms ? ctas : (long long)norm_resident(kernel, g.threads, 0) * sms);
-        kernel<<<grid, g.threads, 0, s>>>(m, a, d, g.tpr);
+        kernel<<<grid, g.threads, 0, s>>>(m, a, d, g.tpr, 1.0f / m.C);
     };
-    if constexpr (V > 1) {
-        switch (g.nv) {
-            case 1: go(wtconv_norm_rows_kernel<T, V, 1, JOIN, Q8>); break;
-            case 2: go(wtconv_norm_rows_kernel<T, V, 2, JOIN, Q8>); break;
-            case 3: go(wtconv_norm_rows_kernel<T, V, 3, JOIN, Q8>); break;
-            case 4: go(wtconv_norm_rows_kernel<T, V, 4, JOIN, Q8>); break;
-            default: go(wtconv_norm_rows_kernel<T, V, 0, JOIN, Q8>); break;
-        }
-    } else {
-        switch (g.nv) {
-            case 4: go(wtconv_norm_rows_kernel<T, V, 4, JOIN, Q8>); break;
-            case 8: go(wtconv_norm_rows_kernel<T, V, 8, JOIN, Q8>); break;
-            case 16: go(wtconv_norm_rows_kernel<T, V, 16, JOIN, Q8>); break;
-            default: go(wtconv_norm_rows_kernel<T, V, 0, JOIN, Q8>); break;
-        }
-    }
+    rows_dispatch<V>(g, [&](auto nv, auto tpr) { go(wtconv_norm_rows_kernel<T, V, nv, tpr, JOIN, Q8>); });
 }
 
 template <typename T, int V>

@@ -10,6 +10,8 @@
 // longer than a CTA's registers: the slots are read again.
 #pragma once
 
+#include <type_traits>
+
 #include "wtconv_norm.cuh"
 
 namespace wtc {
@@ -21,36 +23,73 @@ struct RowsGeom {
     int tpr, nv, threads, step;  // step: rows a CTA holds at once
 };
 
-// Slots of a thread that kernels exist for: 1 to 4 chunks, or 4, 8 or 16 single
-// channels (in fours, since a random word quad covers four).
-inline int rows_nv(int slots, int tpr, int V) {
-    const int n = (slots + tpr - 1) / tpr;
-    if (V > 1) return n <= 4 ? n : 0;
-    return n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : 0;
-}
+// Teams of single channels, for which kernels exist with the width at compile
+// time (the offsets of a thread's slots are then constants): the narrowest that
+// holds a row, since the work for each row weighs more than that for a slot.
+// The last two are CTAs of any width.
+struct SingleTeam {
+    int nv, tpr;
+};
+constexpr SingleTeam kSingles[] = {{4, 8}, {8, 8}, {8, 16}, {8, 32}, {16, 32}, {8, 0}, {16, 0}};
 
-// The part of a warp (at least `least` threads) that leaves the fewest slots
-// empty, and of those the widest, which holds the fewest registers: 24 slots
-// are 8 x 3, 64 are 32 x 2.  Longer rows take a CTA.
-inline RowsGeom rows_geom(const MapShape& m, int V, int least, int sms) {
+// Chunks: the part of a warp (at least `least` threads, and four: 64 adjacent
+// bytes) that leaves the fewest slots empty, and of those the widest, which
+// holds the fewest registers: 24 slots are 8 x 3, 64 are 32 x 2.  Longer rows
+// take a CTA.  warp: no team wider than a warp.
+inline RowsGeom rows_geom(const MapShape& m, int V, int least, bool warp, int sms) {
     const int slots = (m.C + V - 1) / V;
     RowsGeom g{};
-    int best = 0;
-    for (int tpr = least; tpr <= 32; tpr *= 2) {
-        const int nv = rows_nv(slots, tpr, V);
-        if (nv && (!best || tpr * nv <= best)) best = tpr * nv, g.tpr = tpr, g.nv = nv;
+    if (V == 1) {
+        for (const SingleTeam& s : kSingles) {
+            const int tpr = s.tpr ? s.tpr : std::min(kMaxTeam, ((slots + s.nv - 1) / s.nv + 31) / 32 * 32);
+            if (tpr < least || (warp && tpr > 32) || tpr * s.nv < slots) continue;
+            g.tpr = tpr, g.nv = s.nv;
+            break;
+        }
+        if (!g.tpr) g.tpr = warp ? 32 : kMaxTeam;
+    } else {
+        int best = 0;
+        for (int tpr = std::max(4, least); tpr <= 32; tpr *= 2) {
+            const int nv = (slots + tpr - 1) / tpr;
+            if (nv <= 4 && (!best || tpr * nv <= best)) best = tpr * nv, g.tpr = tpr, g.nv = nv;
+        }
+        if (!best) {
+            g.tpr = std::min(kMaxTeam, ((slots + 3) / 4 + 31) / 32 * 32);
+            g.nv = (slots + g.tpr - 1) / g.tpr;
+            if (g.nv > 4) g.nv = 0;
+        }
     }
-    if (best) {
+    g.threads = g.tpr;
+    if (g.tpr <= 32) {
         g.threads = kTeamThreads;
         while (g.threads > 32 && (long long)(g.threads / 2 / g.tpr) * sms >= m.rows) g.threads /= 2;  // few rows: spread them
-    } else {
-        const int most = V > 1 ? 4 : 16;
-        g.tpr = std::min(kMaxTeam, ((slots + most - 1) / most + 31) / 32 * 32);
-        g.nv = rows_nv(slots, g.tpr, V);
-        g.threads = g.tpr;
     }
     g.step = g.threads / g.tpr;
     return g;
+}
+
+// go(nv, tpr) with the geometry's numbers as constants (tpr 0: a runtime one).
+template <int V, typename F>
+void rows_dispatch(const RowsGeom& g, F go) {
+    using std::integral_constant;
+    constexpr integral_constant<int, 0> any{};
+    if constexpr (V > 1) {
+        switch (g.nv) {
+            case 1: return go(integral_constant<int, 1>{}, any);
+            case 2: return go(integral_constant<int, 2>{}, any);
+            case 3: return go(integral_constant<int, 3>{}, any);
+            case 4: return go(integral_constant<int, 4>{}, any);
+        }
+    } else {
+        if (g.nv == 4 && g.tpr == 8) return go(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+        if (g.nv == 8 && g.tpr == 8) return go(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+        if (g.nv == 8 && g.tpr == 16) return go(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+        if (g.nv == 8 && g.tpr == 32) return go(integral_constant<int, 8>{}, integral_constant<int, 32>{});
+        if (g.nv == 16 && g.tpr == 32) return go(integral_constant<int, 16>{}, integral_constant<int, 32>{});
+        if (g.nv == 8) return go(integral_constant<int, 8>{}, any);
+        if (g.nv == 16) return go(integral_constant<int, 16>{}, any);
+    }
+    go(any, any);
 }
 
 // Sum (or largest bits) over a team; `red` holds one value a warp.

@@ -9,10 +9,16 @@ namespace wtc {
 
 namespace {
 
-template <typename T, int V, int NV, bool DROP>
-__global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape m, NormBwdArgs a, MapDrop d, int tpr) {
+template <typename T, int V, int NV, int TPR, bool DROP>
+__global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape m, NormBwdArgs a, MapDrop d, int team, float per_channel) {
+    const int tpr = TPR ? TPR : team;
     using R = typename Chunk<T, V>::type;
     constexpr int NR = NV ? NV : V == 1 ? 4 : 1;
+    // Slots past a row's end hold zeros, and are passed over by a branch or
+    // computed all the same.  No branch lets all loads start first, at the price
+    // of registers: 96 fp32 channels 36 us without, 40 with it (32 x 56 x 56, with
+    // dh), but 512 bf16 ones 116 and 103 us, and 512 fp32 with dropout 230 and 212.
+    constexpr bool kSkip = !NV || V == 8 || (V == 4 && DROP);
     __shared__ float red[kMaxTeam / 32];
     extern __shared__ float sums[];  // [warps][C] at the end, for teams within a warp
     const int t = threadIdx.x % tpr, step = blockDim.x / tpr, slots = (m.C + V - 1) / V;
@@ -64,7 +70,7 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
             float sum[V] = {};
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-                if (!in(i0 + i)) continue;
+                if (kSkip && !in(i0 + i)) continue;
                 float fh[V], fg[V];
                 unpack(hr[i], fh);
                 unpack(gr[i], fg);
@@ -85,7 +91,7 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
         }
         if (!a.dres && !(DROP && a.dx)) continue;
         gh = team_sum(gh, tpr, red);
-        const float s = -(gh / m.C) * r * r * r;  // dres = dh + (r * w) * dy + s * h
+        const float s = -(gh * per_channel) * r * r * r;  // dres = dh + (r * w) * dy + s * h
         auto out = [&](int i0) {
             if (!NV) load(i0), load_dh(i0);
             float fe[NR][V];
@@ -93,7 +99,7 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
             for (int i = 0; i < NR; ++i) {
                 const int c = ((i0 + i) * tpr + t) * V;
                 unpack(er[i], fe[i]);
-                if (!in(i0 + i)) continue;
+                if (kSkip && !in(i0 + i)) continue;
                 float fh[V], fg[V];
                 unpack(hr[i], fh);
                 unpack(gr[i], fg);
@@ -101,7 +107,7 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
                 mul_n(fg, w[i]);
                 fma_n(fg, r, fe[i]);
                 fma_n(fh, s, fe[i]);
-                if (a.dres) *reinterpret_cast<R*>(static_cast<T*>(a.dres) + base + c) = Chunk<T, V>::from(fe[i]);
+                if (a.dres && in(i0 + i)) *reinterpret_cast<R*>(static_cast<T*>(a.dres) + base + c) = Chunk<T, V>::from(fe[i]);
             }
             if (DROP && a.dx) {
                 float g[NR][V] = {};
@@ -155,30 +161,18 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
 // The number of partial vectors, or 0 if there are none (NV = 0).
 template <typename T, int V, bool DROP>
 int run(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
-    const RowsGeom g = rows_geom(m, V, 4, sms);
+    const RowsGeom g = rows_geom(m, V, 0, false, sms);
     const long long ctas = std::min((m.rows + g.step - 1) / g.step, norm_parts(m, sms));
-    const size_t smem = g.tpr <= 32 && g.threads > 32 && a.dweight ? (size_t)(g.threads / 32) * m.C * 4 : 0;
-    auto go = [&](auto kernel, size_t bytes) {
-        const unsigned grid = (unsigned)std::min(ctas, ctas <= 2LL * sms ? ctas : (long long)norm_resident(kernel, g.threads, bytes) * sms);
-        kernel<<<grid, g.threads, bytes, s>>>(m, a, d, g.tpr);
-        return (int)grid;
-    };
-    if constexpr (V > 1) {
-        switch (g.nv) {
-            case 1: return go(wtconv_norm_rows_bwd_kernel<T, V, 1, DROP>, smem);
-            case 2: return go(wtconv_norm_rows_bwd_kernel<T, V, 2, DROP>, smem);
-            case 3: return go(wtconv_norm_rows_bwd_kernel<T, V, 3, DROP>, smem);
-            case 4: return go(wtconv_norm_rows_bwd_kernel<T, V, 4, DROP>, smem);
-        }
-    } else {
-        switch (g.nv) {
-            case 4: return go(wtconv_norm_rows_bwd_kernel<T, V, 4, DROP>, smem);
-            case 8: return go(wtconv_norm_rows_bwd_kernel<T, V, 8, DROP>, smem);
-            case 16: return go(wtconv_norm_rows_bwd_kernel<T, V, 16, DROP>, smem);
-        }
-    }
-    if (a.dres || a.dx) go(wtconv_norm_rows_bwd_kernel<T, V, 0, DROP>, 0);
-    return 0;
+    const size_t smem = g.nv && g.tpr <= 32 && g.threads > 32 && a.dweight ? (size_t)(g.threads / 32) * m.C * 4 : 0;
+    int parts = 0;
+    rows_dispatch<V>(g, [&](auto nv, auto tpr) {
+        if (nv == 0 && !a.dres && !a.dx) return;
+        auto kernel = wtconv_norm_rows_bwd_kernel<T, V, nv, tpr, DROP>;
+        const unsigned grid = (unsigned)std::min(ctas, ctas <= 2LL * sms ? ctas : (long long)norm_resident(kernel, g.threads, smem) * sms);
+        kernel<<<grid, g.threads, smem, s>>>(m, a, d, g.tpr, 1.0f / m.C);
+        if (nv) parts = (int)grid;
+    });
+    return parts;
 }
 
 template <typename T>
