@@ -20,6 +20,8 @@
 // The squares are summed over an owner's channels, the lanes, then the warps
 // (tile_sum).  The weight gradient's sums of a thread's own channels stay in
 // its registers for all its tiles.
+#include <type_traits>
+
 #include "wtconv_norm_planes.cuh"
 
 namespace wtc {
@@ -30,7 +32,8 @@ constexpr int kMaxWarps = 16;
 constexpr int kSmem = 200 * 1024;      // of the 227 KB a CTA may have
 constexpr int kSmemTwo = 104 * 1024;   // two CTAs an SM, with their sums
 
-constexpr int kRagged = 4;  // pixels of a thread where planes are ragged
+constexpr int kRagged = 4;       // pixels of a thread where planes are ragged
+constexpr int kRaggedLanes = 16;  // lanes along them, at compile time (constant offsets), unless that does not fit
 
 struct PlanesGeom {
     int lp, warps, owners, iters;  // iters: quads of an owner
@@ -43,21 +46,21 @@ struct PlanesGeom {
     float per_channel;             // 1 / C
 };
 
-// Tiles of 128 bytes of a plane (256 where it is ragged, so that the chunks at
-// their ends weigh less), less where two stages of `tensors` tensors do not
+// Tiles of 128 bytes of a plane (64 pixels where it is ragged), less where two stages of `tensors` tensors do not
 // leave room for two CTAs on an SM, down to 64 bytes, and then what fits at
 // all.  False if nothing does.
 bool planes_geom(const MapShape& m, int VP, bool ragged, int esize, int tensors, PlanesGeom* out) {
     if ((long long)m.C * m.HW >= 1LL << 31) return false;  // offsets within a sample are 32-bit
     const int quads = (m.C + 3) / 4;
-    int lp = ragged ? 64 / esize : 8;
-    while (lp < 32 && quads * lp <= 16) lp *= 2;
+    int lp = ragged ? kRaggedLanes : 8;
+    while (!ragged && lp < 32 && quads * lp <= 16) lp *= 2;
     while (lp > 1 && lp / 2 * VP >= m.HW) lp /= 2;
     for (; lp >= 1; lp /= 2) {
         PlanesGeom g{};
         const int lanes = 32 / lp;
         g.lp = lp;
-        g.iters = 1;
+        // Two quads an owner where one needs too many warps (ragged: where that leaves four, for less work around a tile).
+        g.iters = ragged && quads >= 2 * 4 * lanes ? 2 : 1;
         while (g.iters < 2 && (quads + lanes * g.iters - 1) / (lanes * g.iters) > kMaxWarps) g.iters *= 2;
         g.warps = (quads + lanes * g.iters - 1) / (lanes * g.iters);
         if (g.warps > kMaxWarps) continue;
@@ -87,7 +90,7 @@ template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
 // Where a thread is: its tile, and its channels' places in it.
-template <typename T, int VP, bool RAG>
+template <typename T, int VP, int RAG>
 struct Tile {
     using R = typename Chunk<T, VP>::type;
 
@@ -101,20 +104,21 @@ struct Tile {
     int live;           // how many of this thread's pixels are the map's
     long long origin;   // the tile's first element
 
+    __device__ __forceinline__ int lp() const { return RAG > 1 ? RAG : geom.lp; }
     __device__ __forceinline__ Tile(const MapShape& shape, const PlanesGeom& g, char* s) : m(shape), geom(g), smem(s) {
         const int lane = threadIdx.x % 32;
-        pl = lane & (geom.lp - 1);
-        owner = (threadIdx.x / 32) * (32 / geom.lp) + lane / geom.lp;
+        pl = lane & (lp() - 1);
+        owner = (threadIdx.x / 32) * (32 / lp()) + lane / lp();
         own = 4u * owner * m.HW + pixel(0);
     }
     // The tile's pixel that is this thread's e-th.
-    __device__ __forceinline__ int pixel(int e) const { return RAG ? pl + e * geom.lp : pl * VP + e; }
+    __device__ __forceinline__ int pixel(int e) const { return RAG ? pl + e * lp() : pl * VP + e; }
     __device__ __forceinline__ void at(long long tile) {
         b = geom.by_tiles(tile);
-        p0 = (int)(tile - b * geom.tiles) * geom.lp * VP;
+        p0 = (int)(tile - b * geom.tiles) * lp() * VP;
         origin = b * m.C * m.HW + p0;
         const int left = m.HW - p0 - pixel(0);  // chunks: HW is a multiple of VP
-        live = !RAG ? (left > 0 ? VP : 0) : left <= 0 ? 0 : min(VP, (left - 1) / geom.lp + 1);
+        live = !RAG ? (left > 0 ? VP : 0) : left <= 0 ? 0 : min(VP, (left - 1) / lp() + 1);
     }
     // This thread's pixels of one value for each of the tile's.
     __device__ __forceinline__ void get(const float* p, float (&v)[VP]) const {
@@ -139,7 +143,8 @@ struct Tile {
     __device__ __forceinline__ uint4 raw(int stage, int tensors, int k, int g, int j) const {
         return reinterpret_cast<const uint4*>(smem + (stage * tensors + k) * geom.tensor)[(4 * g + j) * blockDim.x + threadIdx.x];
     }
-    // This thread's pixels of channel(g, j) of tensor k of a stage, as floats.
+    // This thread's pixels of channel(g, j) of tensor k of a stage, as floats;
+    // ragged: anything for those that it does not have.
     __device__ __forceinline__ void load(int stage, int tensors, int k, int g, int j, float (&f)[VP]) const {
         if constexpr (RAG) {
             const char* s = smem + (stage * tensors + k) * geom.tensor;
@@ -147,7 +152,7 @@ struct Tile {
             const uint32_t first = ((uint32_t)origin + (uint32_t)c * m.HW) * (uint32_t)sizeof(T);  // modulo 2^32
             const T* p = reinterpret_cast<const T*>(s + c * geom.row + (first & 15)) + pl;
 #pragma unroll
-            for (int e = 0; e < VP; ++e) f[e] = e < live ? to_f(p[e * geom.lp]) : 0.0f;
+            for (int e = 0; e < VP; ++e) f[e] = to_f(p[e * lp()]);
         } else {
             unpack(raw(stage, tensors, k, g, j), f);
         }
@@ -158,7 +163,7 @@ struct Tile {
         if constexpr (RAG) {
 #pragma unroll
             for (int e = 0; e < VP; ++e)
-                if (e < live) p[e * geom.lp] = from_f<T>(f[e]);
+                if (e < live) p[e * lp()] = from_f<T>(f[e]);
         } else {
             *reinterpret_cast<R*>(p) = pack(f);
         }
@@ -171,7 +176,7 @@ struct Tile {
         } else {
 #pragma unroll
             for (int e = 0; e < VP; ++e) {
-                const uint4 u = drop_words(d, off, row() + e * geom.lp, quad);
+                const uint4 u = drop_words(d, off, row() + e * lp(), quad);
                 if (u.x >= d.thresh) r[0][e] = __fmaf_rn(f[0][e], d.grown, r[0][e]);
                 if (u.y >= d.thresh) r[1][e] = __fmaf_rn(f[1][e], d.grown, r[1][e]);
                 if (u.z >= d.thresh) r[2][e] = __fmaf_rn(f[2][e], d.grown, r[2][e]);
@@ -186,7 +191,7 @@ struct Tile {
         char* s = smem + stage * tensors * geom.tensor;
         if constexpr (RAG) {
             const long long bytes = m.rows * m.C * (long long)sizeof(T);
-            const int pixels = min(geom.lp * VP, m.HW - p0), chunks = geom.row / 16;
+            const int pixels = min(lp() * VP, m.HW - p0), chunks = geom.row / 16;
             const int n = m.C * chunks;
             for (int i = threadIdx.x; i < n; i += blockDim.x) {
                 const int c = (int)((__umulhi((uint32_t)i, geom.by_chunks.mul) + (uint32_t)i) >> geom.by_chunks.shift);
@@ -229,7 +234,7 @@ struct Tile {
 // its result.  smem: [warps + 1][lp * VP] floats.
 template <int VP, typename Tl, typename F>
 __device__ __forceinline__ void tile_sum(const Tl& tile, float (&v)[VP], float* smem, F finish) {
-    const int lp = tile.geom.lp, warps = blockDim.x / 32, lane = threadIdx.x % 32, px = lp * VP;
+    const int lp = tile.lp(), warps = blockDim.x / 32, lane = threadIdx.x % 32, px = lp * VP;
     for (int o = lp; o < 32; o *= 2) {
 #pragma unroll
         for (int e = 0; e < VP; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
@@ -249,14 +254,14 @@ __device__ __forceinline__ void tile_sum(const Tl& tile, float (&v)[VP], float* 
 }
 
 // h between the sum and the output: as stored, or as the floats that it stands for.
-template <typename T, int VP, bool RAG>
-struct Held {
+template <typename T, int VP>
+struct HeldChunk {
     typename Chunk<T, VP>::type v;
     __device__ __forceinline__ void put(float (&f)[VP]) { v = pack(f), unpack(v, f); }
     __device__ __forceinline__ void get(float (&f)[VP]) const { unpack(v, f); }
 };
 template <typename T, int VP>
-struct Held<T, VP, true> {
+struct HeldFloats {
     float v[VP];
     __device__ __forceinline__ void put(float (&f)[VP]) {
 #pragma unroll
@@ -268,16 +273,19 @@ struct Held<T, VP, true> {
     }
 };
 
+template <typename T, int VP, int RAG>
+using Held = std::conditional_t<RAG != 0, HeldFloats<T, VP>, HeldChunk<T, VP>>;
+
 // G: quads of an owner (geom.iters), at compile time for what stays in registers.
-template <typename T, int VP, bool RAG, int G, int JOIN, bool Q8>
+template <typename T, int VP, int RAG, int G, int JOIN, bool Q8>
 __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapShape m, NormFwdArgs a, MapDrop d, PlanesGeom geom) {
     constexpr int NT = JOIN == kPlain ? 1 : 2;
     extern __shared__ __align__(16) char smem[];  // two stages; tile_sum's; (Q8) the groups' largest bits: [groups][px]
     float* sums = reinterpret_cast<float*>(smem + geom.head);
-    const int px = geom.lp * VP, warps = blockDim.x / 32;
+    Tile<T, VP, RAG> now(m, geom, smem), next(m, geom, smem);
+    const int px = now.lp() * VP, warps = blockDim.x / 32;
     const uint32_t offset = JOIN == kDropped ? drop_offset(d) : 0;
     const long long total = m.rows / m.HW * geom.tiles;
-    Tile<T, VP, RAG> now(m, geom, smem), next(m, geom, smem);
     auto fetch = [&](const Tile<T, VP, RAG>& t, int stage) {
         bool skip = false;
         if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) skip = !keep_sample(d, offset, t.b);
@@ -375,12 +383,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
                     for (int e = 0; e < VP; ++e) bits[e] = max(bits[e], abs_bits(f[e]));
                 }
                 // The lanes of a group first, then one of them to shared memory.
-                int o = geom.lp;
-                for (; o < 32 && o / geom.lp * 4 < a.group; o *= 2) {
+                int o = now.lp();
+                for (; o < 32 && o / now.lp() * 4 < a.group; o *= 2) {
 #pragma unroll
                     for (int e = 0; e < VP; ++e) bits[e] = max(bits[e], __shfl_xor_sync(0xffffffffu, bits[e], o));
                 }
-                if (now.in(g, 0) && (threadIdx.x & (o - 1) & ~(geom.lp - 1)) == 0) {
+                if (now.in(g, 0) && (threadIdx.x & (o - 1) & ~(now.lp() - 1)) == 0) {
 #pragma unroll
                     for (int e = 0; e < VP; ++e)
                         if (now.has(e)) atomicMax(&top[now.channel(g, 0) / a.group * px + now.pixel(e)], bits[e]);
@@ -409,7 +417,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
                     if constexpr (RAG) {
 #pragma unroll
                         for (int e = 0; e < VP; ++e)
-                            if (now.has(e)) q[e * geom.lp] = q8_one(f[e], a.q8);
+                            if (now.has(e)) q[e * now.lp()] = q8_one(f[e], a.q8);
                     } else {
                         q8_store<VP>(q, f, a.q8);
                     }
@@ -420,7 +428,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
     }
 }
 
-template <typename T, int VP, bool RAG, int G, bool DROP>
+template <typename T, int VP, int RAG, int G, bool DROP>
 __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(MapShape m, NormBwdArgs a, MapDrop d, PlanesGeom geom) {
     extern __shared__ __align__(16) char smem[];
     float* sums = reinterpret_cast<float*>(smem + geom.head);
@@ -462,6 +470,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
                 now.load(stage, NT, 0, g, j, fh);
                 now.load(stage, NT, 1, g, j, fg);
                 mul_n(fg, fh);
+                if (RAG) {  // what lies past a plane's end is another plane's, or nothing
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) fg[e] = now.has(e) ? fg[e] : 0.0f;
+                }
                 fma_n(fg, w[g][j], gh);
                 fma_n(fg, r, own);
 #pragma unroll
@@ -511,12 +523,25 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float v = acc[g][j];
-                for (int o = 1; o < geom.lp; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+                for (int o = 1; o < now.lp(); o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
                 const int c = now.channel(g, j);
                 if (now.pl == 0 && c < m.C) part[c] = v;
             }
         }
     }
+}
+
+// go(RAG, G) with the geometry's numbers as constants (RAG 1: a runtime lp).
+template <int RAG, typename F>
+int planes_dispatch(const PlanesGeom& g, F go) {
+    using std::integral_constant;
+    constexpr integral_constant<int, 1> one{};
+    constexpr integral_constant<int, 2> two{};
+    if constexpr (RAG != 0) {
+        if (g.lp != RAG) return g.iters == 1 ? go(one, one) : go(one, two);
+    }
+    constexpr integral_constant<int, RAG> rag{};
+    return g.iters == 1 ? go(rag, one) : go(rag, two);
 }
 
 // Launches a kernel on at most `most` CTAs, as many as the SMs hold at once.
@@ -530,19 +555,20 @@ int launch(K kernel, const MapShape& m, const A& a, const MapDrop& d, const Plan
     return (int)ctas;
 }
 
-template <typename T, int VP, bool RAG, int JOIN, bool Q8>
+template <typename T, int VP, int RAG, int JOIN, bool Q8>
 bool run_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     PlanesGeom g;
     if (!planes_geom(m, VP, RAG, sizeof(T), JOIN == kPlain ? 1 : 2, &g)) return false;
     const int groups = Q8 ? (m.C + a.group - 1) / a.group : 0;
     const size_t smem = g.head + (size_t)(g.warps + 1 + groups) * g.lp * VP * 4;
     if (smem > 225 * 1024) return false;
-    if (g.iters == 1) launch(wtconv_norm_planes_kernel<T, VP, RAG, 1, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
-    else launch(wtconv_norm_planes_kernel<T, VP, RAG, 2, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
+    planes_dispatch<RAG>(g, [&](auto rag, auto quads) {
+        return launch(wtconv_norm_planes_kernel<T, VP, rag, quads, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
+    });
     return true;
 }
 
-template <typename T, int VP, bool RAG>
+template <typename T, int VP, int RAG>
 bool pick_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     if (a.q8 >= 0)
         return a.residual ? run_fwd<T, VP, RAG, kResidual, true>(m, a, d, sms, s) : run_fwd<T, VP, RAG, kPlain, true>(m, a, d, sms, s);
@@ -561,18 +587,19 @@ template <typename T>
 bool fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     constexpr int V = kVec<T>;
     if (!aligned({a.x, a.residual})) return false;
-    if (m.HW % V == 0 && aligned({a.h}) && (uintptr_t)a.y % (a.q8 >= 0 ? V : 16) == 0) return pick_fwd<T, V, false>(m, a, d, sms, s);
-    return pick_fwd<T, kRagged, true>(m, a, d, sms, s);
+    if (m.HW % V == 0 && aligned({a.h}) && (uintptr_t)a.y % (a.q8 >= 0 ? V : 16) == 0) return pick_fwd<T, V, 0>(m, a, d, sms, s);
+    return pick_fwd<T, kRagged, kRaggedLanes>(m, a, d, sms, s);
 }
 
-template <typename T, int VP, bool RAG, bool DROP>
+template <typename T, int VP, int RAG, bool DROP>
 int run_bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     PlanesGeom g;
     if (!planes_geom(m, VP, RAG, sizeof(T), a.dh ? 3 : 2, &g)) return 0;
     const size_t smem = g.head + (size_t)(g.warps + 1) * g.lp * VP * 4;
     const long long most = norm_parts(m, sms);
-    return g.iters == 1 ? launch(wtconv_norm_planes_bwd_kernel<T, VP, RAG, 1, DROP>, m, a, d, g, smem, most, sms, s)
-                        : launch(wtconv_norm_planes_bwd_kernel<T, VP, RAG, 2, DROP>, m, a, d, g, smem, most, sms, s);
+    return planes_dispatch<RAG>(g, [&](auto rag, auto quads) {
+        return launch(wtconv_norm_planes_bwd_kernel<T, VP, rag, quads, DROP>, m, a, d, g, smem, most, sms, s);
+    });
 }
 
 // The number of partial vectors, or 0 if the map is not one for these kernels.
@@ -581,8 +608,8 @@ int bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cuda
     constexpr int V = kVec<T>;
     if (!aligned({a.h, a.dy, a.dh})) return 0;
     if (m.HW % V == 0 && aligned({a.dres, a.dx}))
-        return a.dx ? run_bwd<T, V, false, true>(m, a, d, sms, s) : run_bwd<T, V, false, false>(m, a, d, sms, s);
-    return a.dx ? run_bwd<T, kRagged, true, true>(m, a, d, sms, s) : run_bwd<T, kRagged, true, false>(m, a, d, sms, s);
+        return a.dx ? run_bwd<T, V, 0, true>(m, a, d, sms, s) : run_bwd<T, V, 0, false>(m, a, d, sms, s);
+    return a.dx ? run_bwd<T, kRagged, kRaggedLanes, true>(m, a, d, sms, s) : run_bwd<T, kRagged, kRaggedLanes, false>(m, a, d, sms, s);
 }
 
 }  // namespace

@@ -251,6 +251,30 @@ def test_infinities_and_nan(layout):
             assert torch.equal(torch.isnan(q.float()), lost.expand(shape))
 
 
+@pytest.mark.parametrize("layout", ["nchw", "nhwc"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 10, 7, 7), (1, 70, 9, 9), (2, 16, 8, 8), (1, 300, 3, 5)], ids=str)
+def test_infinite_values_stay_in_their_channel(shape, dtype, layout):
+    # The first and last pixels of one channel's plane: what a kernel reads beyond a plane's or row's end must not
+    # reach its neighbours' sums.
+    gen = gen_of("inf", shape, layout)
+    h, dy = make(shape, layout, dtype, gen), make(shape, layout, dtype, gen)
+    w = torch.ones(shape[1], device="cuda")
+    rstd = torch.ones(shape[0], shape[2], shape[3], device="cuda")
+    c = 5
+    for b in range(shape[0]):
+        for y, x in ((0, 0), (0, 1), (shape[2] - 1, shape[3] - 1)):
+            dy[b, c, y, x] = float("nan")
+            h[b, c + 2, y, x] = float("inf")
+    dx, _, dw = wt.rms_norm_backward(h, dy, w, rstd)
+    bad = torch.zeros(shape[1], dtype=torch.bool, device="cuda")
+    bad[[c, c + 2]] = True
+    assert torch.equal(~torch.isfinite(dw), bad)
+    pixels = torch.zeros_like(rstd, dtype=torch.bool)
+    pixels[:, 0, :2] = pixels[:, -1, -1] = True
+    assert torch.equal(torch.isfinite(dx).all(dim=1), ~pixels)
+
+
 def test_zero_rows_and_the_largest_values():
     x = torch.zeros(3, 40, device="cuda")
     w = torch.ones(40, device="cuda")
