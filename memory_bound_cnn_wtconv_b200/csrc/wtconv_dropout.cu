@@ -7,7 +7,8 @@
 // what it draws:
 //   rows    channels adjacent: a 16-byte chunk of channels (one or two quads);
 //   planes  pixels adjacent: a 16-byte chunk of pixels of four channels (one
-//           quad a pixel), or single pixels where planes are not whole chunks;
+//           quad a pixel);
+//   ragged  the same where planes are not whole chunks, pixel by pixel;
 //   spans   whole stretches of memory under one decision (samples in either
 //           layout, channels of NCHW): x is not read where it is dropped.
 #include <algorithm>
@@ -68,38 +69,84 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_rows_kernel(MapShape 
     }
 }
 
-template <typename T, int VP, bool RES>
+template <typename T, bool RES>
 __global__ void __launch_bounds__(kThreads) wtconv_dropout_planes_kernel(MapShape m, DropArgs a, MapDrop d, Divide by_chunks, Divide by_quads) {
-    using R = typename Chunk<T, VP>::type;
+    constexpr int V = kVec<T>;
     const int quads = (int)by_quads.d, chunks = (int)by_chunks.d;
-    const long long n = m.rows / VP * quads, step = (long long)gridDim.x * kThreads;
+    const long long n = m.rows / V * quads, step = (long long)gridDim.x * kThreads;
     const uint32_t offset = drop_offset(d);
     for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
         const long long bq = by_chunks(i), b = by_quads(bq);
-        const int p = (int)(i - bq * chunks) * VP, quad = (int)(bq - b * quads);
+        const int p = (int)(i - bq * chunks) * V, quad = (int)(bq - b * quads);
         const long long base = (b * m.C + 4 * quad) * m.HW + p;
         const T* x = static_cast<const T*>(a.x) + base;
         const T* res = static_cast<const T*>(a.residual) + base;
-        R rx[4], rr[4];
+        uint4 rx[4], rr[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool in = 4 * quad + j < m.C;
-            rx[j] = in ? *reinterpret_cast<const R*>(x + (long long)j * m.HW) : Chunk<T, VP>::zero();
-            rr[j] = RES && in ? *reinterpret_cast<const R*>(res + (long long)j * m.HW) : Chunk<T, VP>::zero();
+            rx[j] = in ? *reinterpret_cast<const uint4*>(x + (long long)j * m.HW) : make_uint4(0, 0, 0, 0);
+            rr[j] = RES && in ? *reinterpret_cast<const uint4*>(res + (long long)j * m.HW) : make_uint4(0, 0, 0, 0);
         }
-        if constexpr (VP > 1) {
-            drop_add_chunks<T>(d, offset, b * m.HW + p, b, quad, rx, rr);
-        } else {
-            float f[4][1], r[4][1];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) unpack(rx[j], f[j]), unpack(rr[j], r[j]);
-            drop_add_tile<1>(d, offset, b * m.HW + p, b, quad, f, r);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) rr[j] = from_f<T>(r[j][0]);
-        }
+        drop_add_chunks<T>(d, offset, b * m.HW + p, b, quad, rx, rr);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (4 * quad + j < m.C) *reinterpret_cast<R*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = rr[j];
+            if (4 * quad + j < m.C) *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = rr[j];
+    }
+}
+
+// Planes that are not whole chunks: four channels of E pixels a thread.  E = 2:
+// a warp has 64 neighbouring pixels, a lane two of them, 32 apart.  E = 1, for
+// small planes: the threads lie along the pixels of all planes, and none idles.
+template <typename T, int E, bool RES>
+__global__ void __launch_bounds__(kThreads) wtconv_dropout_ragged_kernel(MapShape m, DropArgs a, MapDrop d, Divide by_chunks, Divide by_quads) {
+    constexpr int kLanes = E == 1 ? 1 : 32;  // threads of a chunk
+    const int quads = (int)by_quads.d, chunks = (int)by_chunks.d;
+    const long long n = m.rows / m.HW * quads * chunks, step = (long long)gridDim.x * (kThreads / kLanes);
+    const uint32_t offset = drop_offset(d);
+    for (long long i = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; i < n; i += step) {
+        const long long bq = by_chunks(i), b = by_quads(bq);
+        const int p = (int)(i - bq * chunks) * kLanes * E + threadIdx.x % kLanes, quad = (int)(bq - b * quads);
+        const long long base = (b * m.C + 4 * quad) * m.HW + p;
+        const T* x = static_cast<const T*>(a.x) + base;
+        const T* res = static_cast<const T*>(a.residual) + base;
+        T rx[4][E], rr[4][E];  // all loads first
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const bool in = 4 * quad + j < m.C && (E == 1 || p + 32 * e < m.HW);
+                rx[j][e] = in ? x[(long long)j * m.HW + 32 * e] : from_f<T>(0.0f);
+                rr[j][e] = RES && in ? res[(long long)j * m.HW + 32 * e] : from_f<T>(0.0f);
+            }
+        }
+        float f[4][E], r[4][E];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[j][e] = to_f(rx[j][e]), r[j][e] = to_f(rr[j][e]);
+        }
+        const bool element = d.mode == WTCONV_DROP_ELEMENT, sample = d.mode == WTCONV_DROP_SAMPLE;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (!element) {
+            u = drop_words(d, offset, b, sample ? 0 : quad);
+            if (sample) u.y = u.z = u.w = u.x;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (element) u = drop_words(d, offset, b * m.HW + p + 32 * e, quad);
+            if (u.x >= d.thresh) r[0][e] = __fmaf_rn(f[0][e], d.grown, r[0][e]);
+            if (u.y >= d.thresh) r[1][e] = __fmaf_rn(f[1][e], d.grown, r[1][e]);
+            if (u.z >= d.thresh) r[2][e] = __fmaf_rn(f[2][e], d.grown, r[2][e]);
+            if (u.w >= d.thresh) r[3][e] = __fmaf_rn(f[3][e], d.grown, r[3][e]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            T* y = static_cast<T*>(a.y) + base + (long long)j * m.HW;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (4 * quad + j < m.C && (E == 1 || p + 32 * e < m.HW)) y[32 * e] = from_f<T>(r[j][e]);
+        }
     }
 }
 
@@ -176,12 +223,18 @@ void run(const MapShape& m, const DropArgs& a, const MapDrop& d, int sms, cudaSt
     } else {
         const int quads = (m.C + 3) / 4;
         const Divide by_quads = divide_by(quads, samples * quads);
-        if (m.HW % V == 0 && whole)
-            wtconv_dropout_planes_kernel<T, V, RES><<<ctas(m.rows / V * quads), kThreads, 0, s>>>(
+        if (m.HW % V == 0 && whole) {
+            wtconv_dropout_planes_kernel<T, RES><<<ctas(m.rows / V * quads), kThreads, 0, s>>>(
                 m, a, d, divide_by(m.HW / V, m.rows / V * quads), by_quads);
-        else
-            wtconv_dropout_planes_kernel<T, 1, RES><<<ctas(m.rows * quads), kThreads, 0, s>>>(
-                m, a, d, divide_by(m.HW, m.rows * quads), by_quads);
+        } else {
+            // Two pixels a lane where a plane has several chunks of 64 (64 x 101 x 57 x 57: bf16 43 us, 47 with one; fp32 41
+            // and 47; four hold too many registers with a residual, fp32 72 us and 51 with two).
+            const int E = m.HW > 256 ? 2 : 1, chunks = E == 1 ? m.HW : (m.HW + 63) / 64;
+            const Divide by_chunks = divide_by(chunks, samples * quads * chunks);
+            const unsigned grid = ctas(samples * quads * chunks * (E == 1 ? 1 : 32));
+            if (E == 2) wtconv_dropout_ragged_kernel<T, 2, RES><<<grid, kThreads, 0, s>>>(m, a, d, by_chunks, by_quads);
+            else wtconv_dropout_ragged_kernel<T, 1, RES><<<grid, kThreads, 0, s>>>(m, a, d, by_chunks, by_quads);
+        }
     }
 }
 
