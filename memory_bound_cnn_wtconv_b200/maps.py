@@ -131,16 +131,16 @@ def _desc(x: torch.Tensor, name: str) -> MapDesc:
 
 def _like(t: torch.Tensor, name: str, x: torch.Tensor, layout: int, dtype=None) -> int:
     """The address of an activation that has to be as x is."""
-    if t.dtype is not (dtype or x.dtype) or t.shape != x.shape or t.device != x.device:
+    if t.dtype is not (dtype or x.dtype) or t.shape != x.shape or t.get_device() != x.get_device():
         raise ValueError(f"{name} must have the shape {tuple(x.shape)}, type {dtype or x.dtype} and device of the input")
-    if not (t.is_contiguous() if layout == NCHW or t.dim() == 2
-            else t.is_contiguous(memory_format=torch.channels_last)):
+    if not t.is_contiguous(memory_format=torch.channels_last if layout == NHWC and t.dim() == 4
+                           else torch.contiguous_format):
         raise ValueError(f"{name} must have the layout of the input ({'NHWC' if layout == NHWC else 'NCHW'})")
     return t.data_ptr()
 
 
 def _vector(t: torch.Tensor, name: str, x: torch.Tensor, shape) -> int:
-    if t.dtype is not torch.float32 or t.device != x.device or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.get_device() != x.get_device() or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor on {x.device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
