@@ -210,7 +210,10 @@ void run(const MapShape& m, const DropArgs& a, const MapDrop& d, int sms, cudaSt
     const bool stretches = !d.on || sample || (d.mode == WTCONV_DROP_CHANNEL && !m.nhwc);
     if (stretches && len >= kLeastSpan) {
         const bool vec = ax == ay && (!RES || ar == ay);
-        const unsigned across = (unsigned)std::min((len / V + kThreads) / kThreads, std::max(1LL, 32LL * sms / spans));
+        // Four chunks a thread (the decision is drawn once for them) where that leaves two CTAs for every SM.
+        const long long chunks = len / V + 1, fours = (chunks + 4 * kThreads - 1) / (4 * kThreads);
+        const long long want = fours * spans >= 2LL * sms ? fours : (chunks + kThreads - 1) / kThreads;
+        const unsigned across = (unsigned)std::min(want, std::max(1LL, 32LL * sms / spans));
         const dim3 grid(across, (unsigned)std::min(spans, std::max(1LL, 32LL * sms / across)));
         wtconv_dropout_spans_kernel<T, RES><<<grid, kThreads, 0, s>>>(m, a, d, spans, len, vec);
     } else if (m.nhwc) {
