@@ -25,8 +25,6 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
             if (i * tpr + t < slots) load_weight<V>(a.weight + (i * tpr + t) * V, w[i]);
         }
     }
-    long long decided = -1;  // the last sample that a decision was drawn for
-    bool kept = true;
     // Every thread of a CTA makes the same number of rounds.
     for (long long row0 = (long long)blockIdx.x * step; row0 < m.rows; row0 += (long long)gridDim.x * step) {
         const long long row = row0 + threadIdx.x / tpr;
@@ -39,10 +37,7 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, 
         bool whole = true;  // a sample's decision
         if (JOIN == kDropped) {
             drow = drop_row(d, row);
-            if (d.mode == WTCONV_DROP_SAMPLE) {  // neighbouring rows are mostly of one sample
-                if (drow != decided) kept = keep_sample(d, offset, drow), decided = drow;
-                whole = kept;
-            }
+            if (d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, drow);
         }
         auto in = [&](int i) { return live && i * tpr + t < slots; };
         R raw[NR];

@@ -19,20 +19,21 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
     // of registers: 96 fp32 channels 36 us without, 40 with it (32 x 56 x 56, with
     // dh), but 512 bf16 ones 116 and 103 us, and 512 fp32 with dropout 230 and 212.
     constexpr bool kSkip = !NV || V == 8 || (V == 4 && DROP);
+    // The weights of a thread's channels stay in registers, but for four bf16 chunks, which then spill: 131072 rows of
+    // 1024 with dh and element dropout 273 us with them, 249 without.
+    constexpr bool kHold = NV && !(V == 8 && NV == 4);
     __shared__ float red[kMaxTeam / 32];
     extern __shared__ float sums[];  // [warps][C] at the end, for teams within a warp
     const int t = threadIdx.x % tpr, step = blockDim.x / tpr, slots = (m.C + V - 1) / V;
     const int iters = NV ? NV : (slots + tpr - 1) / tpr;
     const uint32_t offset = DROP ? drop_offset(d) : 0;
     float acc[NR][V] = {}, w[NR][V] = {};  // of this thread's channels, for all its rows
-    if (NV) {
+    if (kHold) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             if (i * tpr + t < slots) load_weight<V>(a.weight + (i * tpr + t) * V, w[i]);
         }
     }
-    long long decided = -1;
-    bool kept = true;
     for (long long row0 = (long long)blockIdx.x * step; row0 < m.rows; row0 += (long long)gridDim.x * step) {
         const long long row = row0 + threadIdx.x / tpr;
         const bool live = row < m.rows;
@@ -45,10 +46,7 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
         bool whole = true;
         if (DROP) {
             drow = drop_row(d, row);
-            if (d.mode == WTCONV_DROP_SAMPLE) {  // neighbouring rows are mostly of one sample
-                if (drow != decided) kept = keep_sample(d, offset, drow), decided = drow;
-                whole = kept;
-            }
+            if (d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, drow);
         }
         auto in = [&](int i) { return live && i * tpr + t < slots; };
         R hr[NR], gr[NR], er[NR];
@@ -74,7 +72,7 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
                 float fh[V], fg[V];
                 unpack(hr[i], fh);
                 unpack(gr[i], fg);
-                if (!NV) load_weight<V>(a.weight + ((i0 + i) * tpr + t) * V, w[i]);
+                if (!kHold) load_weight<V>(a.weight + ((i0 + i) * tpr + t) * V, w[i]);
                 mul_n(fg, fh);
                 fma_n(fg, w[i], sum);
                 if (NV) fma_n(fg, r, acc[i]);
@@ -103,7 +101,7 @@ __global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape
                 float fh[V], fg[V];
                 unpack(hr[i], fh);
                 unpack(gr[i], fg);
-                if (!NV) load_weight<V>(a.weight + c, w[i]);
+                if (!kHold) load_weight<V>(a.weight + c, w[i]);
                 mul_n(fg, w[i]);
                 fma_n(fg, r, fe[i]);
                 fma_n(fh, s, fe[i]);
