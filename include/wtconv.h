@@ -241,6 +241,7 @@ wtconv_status_t wtconv_backward_weight_noalloc(const wtconv_desc_t *d, const voi
  *   - Results do not depend on the order in which CTAs run: repeated calls
  *     return the same bits.
  *   - Arithmetic is float32.
+ *   - Calls that may run at the same time need workspaces of their own.
  * ------------------------------------------------------------------------ */
 typedef struct {
     int B, C, H, W;

@@ -9,11 +9,12 @@
 
 namespace wtc {
 
-// CTAs per SM of the weight gradient's partial sums, at most (the workspace
-// holds one vector of C floats for each).
-constexpr int kNormParts = 8;
-
-inline long long norm_parts(const MapShape& m, int sms) { return std::min(m.rows, (long long)kNormParts * sms); }
+// CTAs of the backward whose partial sums of the weight gradient the workspace
+// holds, one vector of C floats for each: eight for every SM, fewer where that
+// is over 32 MB, but 64.
+inline long long norm_parts(const MapShape& m, int sms) {
+    return std::min(m.rows, std::max(64LL, std::min(8LL * sms, (1LL << 23) / m.C)));
+}
 
 // CTAs of a kernel that an SM holds.
 template <typename K>

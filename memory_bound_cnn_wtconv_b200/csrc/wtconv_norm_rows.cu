@@ -8,8 +8,17 @@ namespace wtc {
 
 namespace {
 
+// Kernels held to the registers (80) that let an SM hold three CTAs: those that
+// would take more and lose little by it (512 bf16 channels, 32 x 64 x 64, with
+// element dropout 104 us, and 118 with two CTAs).
+template <int V, int NV, int TPR, int JOIN, bool Q8>
+constexpr bool kThree = kWithinWarp<V, NV, TPR> && (V == 8   ? (NV == 2 && JOIN == kDropped) || (NV == 3 && Q8)
+                                                    : V == 4 ? NV == 3 && JOIN == kDropped
+                                                             : NV == 8);
+
 template <typename T, int V, int NV, int TPR, int JOIN, bool Q8>
-__global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_kernel(MapShape m, NormFwdArgs a, MapDrop d, int team, float per_channel) {
+__global__ void __launch_bounds__(kThree<V, NV, TPR, JOIN, Q8> ? kTeamThreads : kMaxTeam, kThree<V, NV, TPR, JOIN, Q8> ? 3 : 0)
+    wtconv_norm_rows_kernel(MapShape m, NormFwdArgs a, MapDrop d, int team, float per_channel) {
     const int tpr = TPR ? TPR : team;
     using R = typename Chunk<T, V>::type;
     // Slots at once: all of them, or for NV = 0 one (four, where quads are exchanged).

@@ -55,8 +55,7 @@ inline RowsGeom rows_geom(const MapShape& m, int V, int least, bool warp, int sm
         }
         if (!best) {
             g.tpr = std::min(kMaxTeam, ((slots + 3) / 4 + 31) / 32 * 32);
-            g.nv = (slots + g.tpr - 1) / g.tpr;
-            if (g.nv > 4) g.nv = 0;
+            g.nv = g.tpr * 4 >= slots ? 4 : 0;
         }
     }
     g.threads = g.tpr;
@@ -67,6 +66,11 @@ inline RowsGeom rows_geom(const MapShape& m, int V, int least, bool warp, int sm
     g.step = g.threads / g.tpr;
     return g;
 }
+
+// Whether a kernel is for teams within a warp only (CTA-wide ones have four
+// chunks or any number of single channels a thread), so for kTeamThreads.
+template <int V, int NV, int TPR>
+constexpr bool kWithinWarp = NV != 0 && (V > 1 ? NV != 4 : TPR != 0);
 
 // go(nv, tpr) with the geometry's numbers as constants (tpr 0: a runtime one).
 template <int V, typename F>

@@ -9,8 +9,16 @@ namespace wtc {
 
 namespace {
 
+// Kernels held to the registers (80) that let an SM hold three CTAs: those that
+// would take more and lose little by it (512 bf16 channels, 32 x 64 x 64, with dh
+// 93 us, and 101 with two CTAs; three bf16 chunks would spill: 96 channels 54 and
+// 38 us).
+template <int V, int NV, int TPR>
+constexpr bool kThree = kWithinWarp<V, NV, TPR> && (V == 8 ? NV == 2 : V == 4 ? NV == 3 : NV == 8);
+
 template <typename T, int V, int NV, int TPR, bool DROP>
-__global__ void __launch_bounds__(kMaxTeam) wtconv_norm_rows_bwd_kernel(MapShape m, NormBwdArgs a, MapDrop d, int team, float per_channel) {
+__global__ void __launch_bounds__(kThree<V, NV, TPR> ? kTeamThreads : kMaxTeam, kThree<V, NV, TPR> ? 3 : 0)
+    wtconv_norm_rows_bwd_kernel(MapShape m, NormBwdArgs a, MapDrop d, int team, float per_channel) {
     const int tpr = TPR ? TPR : team;
     using R = typename Chunk<T, V>::type;
     constexpr int NR = NV ? NV : V == 1 ? 4 : 1;

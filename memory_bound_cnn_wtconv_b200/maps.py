@@ -9,7 +9,10 @@ bfloat16 on one CUDA device; the activations of a call share shape, layout and
 type.  Any size is taken, odd ones and B = 0 too.
 
 A call runs on ``stream`` if given (what it allocates then belongs to that
-stream), else on the current stream of the activations' device.  Everything
+stream), else on the current stream of the activations' device.  Calls that may
+run at the same time need workspaces of their own, as the allocated ones are.
+In CUDA graphs: capture the ``*_forward`` / ``*_backward`` calls, or the
+autograd forms with ``torch.autograd.grad``.  Everything
 runs in the CUDA kernels of ``libwtconv_b200.so``; there is no CPU fallback.
 """
 from __future__ import annotations
@@ -478,7 +481,9 @@ class BranchDropout(torch.nn.Module):
     the next step as its offset.  ``next_drop()`` is that call's ``Drop``, for a
     fused norm.  With ``capturable`` the step is a CUDA tensor which the calls
     move on, so every replay of a captured graph draws new masks.  Seed and
-    step are part of the state dict.
+    step are part of the state dict.  Where a forward is run again for its
+    backward (activation checkpointing), take ``next_drop()`` outside and pass it
+    to ``dropout`` or ``rms_norm``: a second call of the module is a new step.
     """
 
     def __init__(self, p: float, mode: str = "element", seed: int = None, capturable: bool = False, device=None):
