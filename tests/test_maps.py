@@ -199,6 +199,44 @@ def test_mask_is_the_same_in_both_layouts_types_and_operators():
     assert torch.equal(rows, wt.dropout_forward(torch.ones(5, 22, 1, 1, device="cuda"), wt.Drop(0.5, "element", 3, 4))[:, :, 0, 0])
 
 
+# Channel counts on both sides of every border at which the kernels hold a row in another way.
+WIDTHS = [2, 4, 9, 16, 31, 32, 33, 40, 63, 64, 65, 96, 127, 128, 129, 192, 255, 256, 257, 320, 384, 511, 512, 513, 640,
+          1000, 1024, 1025, 1536, 2048, 2049, 4096, 4097, 8191, 8192, 8193, 16384, 16385, 16392]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("layout,hw", [("rows", (1, 1)), ("nchw", (2, 8)), ("nchw", (1, 7)), ("nchw", (3, 43))])
+def test_every_width(layout, hw, dtype):
+    for C in WIDTHS:
+        shape = (3 if layout == "rows" else 1, C, *hw)
+        gen = gen_of("width", C, layout, hw)
+        x, res, dy = (make(shape, layout, dtype, gen) for _ in range(3))
+        w = torch.randn(C, generator=gen).cuda()
+        drop = wt.Drop(0.3, "element", C, 1)
+        y, h, rstd = wt.rms_norm_forward(x, w, res, drop, EPS)
+        check_forward(x, res, w, drop, y, h, rstd)
+        check_backward(h, dy, None, w, drop, *wt.rms_norm_backward(h, dy, w, rstd, None, drop))
+        check_backward(h, dy, res, w, None, *wt.rms_norm_backward(h, dy, w, rstd, res))
+        for group in (0, 32, 128):
+            q, scale, _ = wt.rms_norm_q8(h, w, None, EPS, torch.int8, group)
+            v, _ = ref.norm(wide(h), w.double().cpu().numpy(), EPS)
+            tol, s = ((C + 1) / 2 + 10) * U, np.repeat(wide(scale), group or C, axis=1)[:, :C]
+            close(wide(scale), np.maximum(ref.group_max(v, group or C) / 127.0, 2.0 ** -126), tol * wide(scale), "scale")
+            close(wide(q) * s, v, 0.5 * s * (1 + 4 * tol) + 4 * tol * np.abs(v), "q")
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 7, 147, 148, 149, 1183, 1185, 5000])
+def test_few_and_many_rows(rows):
+    # Row counts around those at which CTAs shrink or start to walk.
+    for C in (6, 24, 96, 520):
+        gen = gen_of("rows", rows, C)
+        x, dy = make((rows, C, 1, 1), "rows", F32, gen), make((rows, C, 1, 1), "rows", F32, gen)
+        w = torch.randn(C, generator=gen).cuda()
+        y, h, rstd = wt.rms_norm_forward(x, w, eps=EPS)
+        check_forward(x, None, w, None, y, h, rstd)
+        check_backward(h, dy, None, w, None, *wt.rms_norm_backward(h, dy, w, rstd))
+
+
 @pytest.mark.parametrize("layout", ["nchw", "nhwc"])
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(2, 96, 8, 8), (1, 40, 16, 4), (1, 1024, 4, 4)], ids=str)
@@ -509,6 +547,56 @@ def test_autograd_refusals():
         step.add_(1)  # the mask of the backward would be another one
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.sum().backward()
+
+
+def test_serving_chain():
+    """The layer, the branch joined to the residual stream, 8-bit activations: q * scale is the norm that training computes."""
+    torch.manual_seed(5)
+    conv, norm = wt.WTConv2d(32, 5, 2, device="cuda"), wt.RMSNorm2d(32, device="cuda")
+    for fmt in (torch.contiguous_format, torch.channels_last):
+        x = torch.randn(2, 32, 16, 16, device="cuda").to(BF16).contiguous(memory_format=fmt)
+        with torch.no_grad():
+            branch = conv(x)
+            y, h = norm(branch, x)
+            for kind, half_step in ((torch.float8_e4m3fn, 2.0 ** -4), (torch.int8, 0.5 / 127)):
+                q, scale, h8 = wt.rms_norm_q8(branch, norm.weight, x, norm.eps, kind)
+                assert torch.equal(h8, h) and h8.stride() == x.stride()
+                got, want = wide(q.float()) * wide(scale), wide(y)
+                # half a step of the 8-bit type (of the pixel's largest value for whole numbers), half a step of bf16
+                size = np.abs(want) if kind != torch.int8 else np.abs(want).max(axis=1, keepdims=True)
+                low = wide(scale) * 2.0 ** -10  # e4m3 below its smallest normal
+                close(got, want, 1.01 * (half_step * size + low + half(BF16) * np.abs(want)), str(kind))
+
+
+def test_captured_autograd_step_of_modules():
+    torch.manual_seed(6)
+    drop = wt.BranchDropout(0.4, "element", seed=9, capturable=True, device="cuda")
+    norm = wt.RMSNorm2d(12, device="cuda")
+    x = torch.randn(2, 12, 5, 6, device="cuda", requires_grad=True)
+    res = torch.randn(2, 12, 5, 6, device="cuda", requires_grad=True)
+    dy = torch.randn(2, 12, 5, 6, device="cuda")
+
+    def call():
+        y, h = norm(x, res, drop.next_drop())
+        return (y, *torch.autograd.grad([y, drop(h)], [x, res, norm.weight], [dy, dy]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = [t.detach() for t in call()]
+    eager = wt.BranchDropout(0.4, "element", seed=9, device="cuda")
+    for _ in range(3):
+        eager.steps = int(drop.step)
+        graph.replay()
+        torch.cuda.synchronize()
+        y, h = norm(x, res, eager.next_drop())
+        want = (y, *torch.autograd.grad([y, eager(h)], [x, res, norm.weight], [dy, dy]))
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert int(drop.step) == 8  # two a call
 
 
 def test_modules():

@@ -121,6 +121,15 @@ def test_workspace(cuda_lib):
         assert bwd(cuda_lib, d, **a, nbytes=need - 4) == bwd(cuda_lib, d, **a, ws=0) == WORKSPACE
 
 
+@pytest.mark.parametrize("C", [1, 96, 4096, 33000, 1 << 20])
+def test_workspace_size(cuda_lib, C):
+    # At most 32 MB, but 64 rows' worth; never more than the map's rows.
+    maps._lib()
+    need = cuda_lib.wtconv_rms_norm_workspace_bytes(ctypes.byref(desc(B=4096, C=C, H=1, W=1)))
+    assert need % (4 * C) == 0 and need <= max(1 << 25, 64 * 4 * C)
+    assert cuda_lib.wtconv_rms_norm_workspace_bytes(ctypes.byref(desc(B=3, C=C, H=1, W=1))) == 3 * 4 * C
+
+
 def test_an_empty_batch_has_nothing_to_do(cuda_lib):
     d = desc(B=0)
     assert fwd(cuda_lib, d, x=0, y=0) == q8(cuda_lib, d, q=0, scale=0) == dropout(cuda_lib, d, drop(), 0, None, 0) == OK
