@@ -69,9 +69,10 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_rows_kernel(MapShape 
     }
 }
 
-template <typename T, bool RES>
+// V: the pixels of a chunk, or of half a one where planes are whole halves only.
+template <typename T, int V, bool RES>
 __global__ void __launch_bounds__(kThreads) wtconv_dropout_planes_kernel(MapShape m, DropArgs a, MapDrop d, Divide by_chunks, Divide by_quads) {
-    constexpr int V = kVec<T>;
+    using R = typename Chunk<T, V>::type;
     const int quads = (int)by_quads.d, chunks = (int)by_chunks.d;
     const long long n = m.rows / V * quads, step = (long long)gridDim.x * kThreads;
     const uint32_t offset = drop_offset(d);
@@ -81,17 +82,17 @@ __global__ void __launch_bounds__(kThreads) wtconv_dropout_planes_kernel(MapShap
         const long long base = (b * m.C + 4 * quad) * m.HW + p;
         const T* x = static_cast<const T*>(a.x) + base;
         const T* res = static_cast<const T*>(a.residual) + base;
-        uint4 rx[4], rr[4];
+        R rx[4], rr[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool in = 4 * quad + j < m.C;
-            rx[j] = in ? *reinterpret_cast<const uint4*>(x + (long long)j * m.HW) : make_uint4(0, 0, 0, 0);
-            rr[j] = RES && in ? *reinterpret_cast<const uint4*>(res + (long long)j * m.HW) : make_uint4(0, 0, 0, 0);
+            rx[j] = in ? *reinterpret_cast<const R*>(x + (long long)j * m.HW) : Chunk<T, V>::zero();
+            rr[j] = RES && in ? *reinterpret_cast<const R*>(res + (long long)j * m.HW) : Chunk<T, V>::zero();
         }
         drop_add_chunks<T>(d, offset, b * m.HW + p, b, quad, rx, rr);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (4 * quad + j < m.C) *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = rr[j];
+            if (4 * quad + j < m.C) *reinterpret_cast<R*>(static_cast<T*>(a.y) + base + (long long)j * m.HW) = rr[j];
     }
 }
 
@@ -226,9 +227,14 @@ void run(const MapShape& m, const DropArgs& a, const MapDrop& d, int sms, cudaSt
     } else {
         const int quads = (m.C + 3) / 4;
         const Divide by_quads = divide_by(quads, samples * quads);
+        auto planes = [&](auto kernel, int chunk) {
+            const long long n = m.rows / chunk * quads;
+            kernel<<<ctas(n), kThreads, 0, s>>>(m, a, d, divide_by(m.HW / chunk, n), by_quads);
+        };
         if (m.HW % V == 0 && whole) {
-            wtconv_dropout_planes_kernel<T, RES><<<ctas(m.rows / V * quads), kThreads, 0, s>>>(
-                m, a, d, divide_by(m.HW / V, m.rows / V * quads), by_quads);
+            planes(wtconv_dropout_planes_kernel<T, V, RES>, V);
+        } else if (m.HW % (V / 2) == 0 && ax % 8 == 0 && ar % 8 == 0 && ay % 8 == 0) {
+            planes(wtconv_dropout_planes_kernel<T, V / 2, RES>, V / 2);
         } else {
             // Two pixels a lane where a plane has several chunks of 64 (64 x 101 x 57 x 57: bf16 43 us, 47 with one; fp32 41
             // and 47; four hold too many registers with a residual, fp32 72 us and 51 with two).

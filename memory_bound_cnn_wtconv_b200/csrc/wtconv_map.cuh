@@ -83,17 +83,41 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// One stored value (pixels whose planes are not whole 16-byte chunks).
+// Half a chunk: eight stored bytes.
+__device__ __forceinline__ void unpack(const uint2& r, float (&f)[2]) { f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y); }
+__device__ __forceinline__ void unpack(const uint2& r, float (&f)[4]) {
+    f[0] = __uint_as_float(r.x << 16), f[1] = __uint_as_float(r.x & 0xffff0000u);
+    f[2] = __uint_as_float(r.y << 16), f[3] = __uint_as_float(r.y & 0xffff0000u);
+}
+
+// One stored value (rows or planes that are not whole chunks).
 __device__ __forceinline__ void unpack(float r, float (&f)[1]) { f[0] = r; }
 __device__ __forceinline__ void unpack(__nv_bfloat16 r, float (&f)[1]) { f[0] = __bfloat162float(r); }
 
-// N stored values as one register group: uint4 for a 16-byte chunk, T for one value.
+// N stored values as one register group: uint4 for a chunk, uint2 for half a one, T for one value.
 template <typename T, int N>
 struct Chunk {
     using type = uint4;
     static __device__ __forceinline__ uint4 zero() { return make_uint4(0, 0, 0, 0); }
     static __device__ __forceinline__ uint4 from(const float (&f)[N]) { return pack(f); }
 };
+template <>
+struct Chunk<float, 2> {
+    using type = uint2;
+    static __device__ __forceinline__ uint2 zero() { return make_uint2(0, 0); }
+    static __device__ __forceinline__ uint2 from(const float (&f)[2]) { return make_uint2(__float_as_uint(f[0]), __float_as_uint(f[1])); }
+};
+template <>
+struct Chunk<__nv_bfloat16, 4> {
+    using type = uint2;
+    static __device__ __forceinline__ uint2 zero() { return make_uint2(0, 0); }
+    static __device__ __forceinline__ uint2 from(const float (&f)[4]) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+        return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+};
+__device__ __forceinline__ uint32_t& word_of(uint4& r, int k) { return k == 0 ? r.x : k == 1 ? r.y : k == 2 ? r.z : r.w; }
+__device__ __forceinline__ uint32_t& word_of(uint2& r, int k) { return k == 0 ? r.x : r.y; }
 template <typename T>
 struct Chunk<T, 1> {
     using type = T;
@@ -156,8 +180,8 @@ __device__ __forceinline__ void drop_add4(const MapDrop& d, const uint4& u, cons
     if (u.z >= d.thresh) r[2] = __fmaf_rn(f[2], d.grown, r[2]);
     if (u.w >= d.thresh) r[3] = __fmaf_rn(f[3], d.grown, r[3]);
 }
-// T(r + d * x) of a 16-byte chunk of pixels of four channels, into r, chunk word
-// by chunk word, so that few values are held as floats at once.
+// T(r + d * x) of a chunk (or half a one) of pixels of four channels, into r, word
+// by word, so that few values are held as floats at once.
 template <typename T>
 __device__ __forceinline__ void drop_add_words(const MapDrop& d, const uint4 (&u)[sizeof(uint32_t) / sizeof(T)], uint32_t x, uint32_t& r, int j) {
     auto word = [&](int v) { return j == 0 ? u[v].x : j == 1 ? u[v].y : j == 2 ? u[v].z : u[v].w; };
@@ -171,9 +195,9 @@ __device__ __forceinline__ void drop_add_words(const MapDrop& d, const uint4 (&u
         r = *reinterpret_cast<const uint32_t*>(&p);
     }
 }
-template <typename T>
+template <typename T, typename R>
 __device__ __forceinline__ void drop_add_chunks(const MapDrop& d, uint32_t offset, long long row, long long b, int quad,
-                                                const uint4 (&x)[4], uint4 (&r)[4]) {
+                                                R (&x)[4], R (&r)[4]) {
     constexpr int N = sizeof(uint32_t) / sizeof(T);  // pixels of a word
     const uint32_t lo = (uint32_t)row, hi = (uint32_t)((unsigned long long)row >> 32);
     uint4 u[N];
@@ -184,16 +208,14 @@ __device__ __forceinline__ void drop_add_chunks(const MapDrop& d, uint32_t offse
         u[N - 1] = u[0];
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < (int)sizeof(R) / 4; ++k) {
         if (element) {
 #pragma unroll
             for (int v = 0; v < N; ++v) u[v] = drop_words(d, offset, lo + k * N + v, hi, quad);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t xk = k == 0 ? x[j].x : k == 1 ? x[j].y : k == 2 ? x[j].z : x[j].w;
-            uint32_t& rk = k == 0 ? r[j].x : k == 1 ? r[j].y : k == 2 ? r[j].z : r[j].w;
-            drop_add_words<T>(d, u, xk, rk, j);
+            drop_add_words<T>(d, u, word_of(x[j], k), word_of(r[j], k), j);
         }
     }
 }

@@ -7,8 +7,9 @@
 //
 // The inputs of the next tile come into shared memory (cp.async, 16 bytes)
 // while this one is computed.  VP = 16 bytes of pixels where planes are whole
-// 16-byte chunks: each thread copies the chunks that it owns itself, so nothing
-// but its own copies has to arrive.  Where they are not (RAG, "ragged"), each
+// 16-byte chunks, 8 where they are whole halves: each thread copies the chunks
+// that it owns itself, so nothing but its own copies has to arrive.  Where they
+// are neither (RAG, "ragged"), each
 // channel's pixels come as the aligned chunks that cover them, shifted by the
 // plane's own distance from a 16-byte boundary, and are read value by value: a
 // thread then has the pixels pl, pl + lp, ..., four of them.
@@ -52,7 +53,7 @@ struct PlanesGeom {
 bool planes_geom(const MapShape& m, int VP, bool ragged, int esize, int tensors, PlanesGeom* out) {
     if ((long long)m.C * m.HW >= 1LL << 31) return false;  // offsets within a sample are 32-bit
     const int quads = (m.C + 3) / 4;
-    int lp = ragged ? kRaggedLanes : 8;
+    int lp = ragged ? kRaggedLanes : 128 / (VP * esize);
     while (!ragged && lp < 32 && quads * lp <= 16) lp *= 2;
     while (lp > 1 && lp / 2 * VP >= m.HW) lp /= 2;
     for (; lp >= 1; lp /= 2) {
@@ -67,7 +68,7 @@ bool planes_geom(const MapShape& m, int VP, bool ragged, int esize, int tensors,
         g.owners = g.warps * lanes;
         g.tiles = (m.HW + lp * VP - 1) / (lp * VP);
         g.row = (lp * VP * esize + 15) / 16 * 16 + 16;
-        const long long tensor = ragged ? (long long)g.row * m.C : 64LL * g.iters * g.warps * 32;
+        const long long tensor = ragged ? (long long)g.row * m.C : 4LL * VP * esize * g.iters * g.warps * 32;
         if (2 * tensors * tensor > kSmem) continue;
         if (2 * tensors * tensor + (g.warps + 1) * lp * VP * 4 > kSmemTwo && lp * VP * esize > 64) continue;
         g.tensor = (int)tensor;
@@ -84,6 +85,10 @@ bool planes_geom(const MapShape& m, int VP, bool ragged, int esize, int tensors,
 __device__ __forceinline__ void copy16(void* to, const void* from, int bytes) {  // the rest of the 16 bytes as zeros
     const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(to));
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy8(void* to, const void* from, int bytes) {
+    const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(to));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(s), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
@@ -125,6 +130,9 @@ struct Tile {
         if constexpr (RAG) {
 #pragma unroll
             for (int e = 0; e < VP; ++e) v[e] = p[pixel(e)];
+        } else if constexpr (VP == 2) {
+            const float2 q = *reinterpret_cast<const float2*>(p + pixel(0));
+            v[0] = q.x, v[1] = q.y;
         } else {
 #pragma unroll
             for (int e = 0; e < VP; e += 4) {
@@ -140,8 +148,8 @@ struct Tile {
     // This thread's first pixel of channel(g, j), from the tile's first element on.
     __device__ __forceinline__ uint32_t offset(int g, int j) const { return own + (uint32_t)(4 * g * geom.owners + j) * m.HW; }
 
-    __device__ __forceinline__ uint4 raw(int stage, int tensors, int k, int g, int j) const {
-        return reinterpret_cast<const uint4*>(smem + (stage * tensors + k) * geom.tensor)[(4 * g + j) * blockDim.x + threadIdx.x];
+    __device__ __forceinline__ R raw(int stage, int tensors, int k, int g, int j) const {
+        return reinterpret_cast<const R*>(smem + (stage * tensors + k) * geom.tensor)[(4 * g + j) * blockDim.x + threadIdx.x];
     }
     // This thread's pixels of channel(g, j) of tensor k of a stage, as floats;
     // ragged: anything for those that it does not have.
@@ -165,7 +173,7 @@ struct Tile {
             for (int e = 0; e < VP; ++e)
                 if (e < live) p[e * lp()] = from_f<T>(f[e]);
         } else {
-            *reinterpret_cast<R*>(p) = pack(f);
+            *reinterpret_cast<R*>(p) = Chunk<T, VP>::from(f);
         }
     }
     // r + dropout of f of quad g, into r.
@@ -213,10 +221,14 @@ struct Tile {
                 for (int j = 0; j < 4; ++j) {
                     const bool ok = in(g, j);
                     const long long at = origin + (ok ? offset(g, j) : 0u);
-                    char* to = s + ((4 * g + j) * blockDim.x + threadIdx.x) * 16;
+                    char* to = s + ((4 * g + j) * blockDim.x + threadIdx.x) * sizeof(R);
 #pragma unroll
-                    for (int k = 0; k < NT; ++k)
-                        if (k < tensors) copy16(to + k * geom.tensor, static_cast<const T*>(from[k]) + at, ok && !(k == 0 && skip) ? 16 : 0);
+                    for (int k = 0; k < NT; ++k) {
+                        if (k >= tensors) continue;
+                        const int bytes = ok && !(k == 0 && skip) ? (int)sizeof(R) : 0;
+                        if constexpr (sizeof(R) == 16) copy16(to + k * geom.tensor, static_cast<const T*>(from[k]) + at, bytes);
+                        else copy8(to + k * geom.tensor, static_cast<const T*>(from[k]) + at, bytes);
+                    }
                 }
             }
         }
@@ -257,7 +269,7 @@ __device__ __forceinline__ void tile_sum(const Tl& tile, float (&v)[VP], float* 
 template <typename T, int VP>
 struct HeldChunk {
     typename Chunk<T, VP>::type v;
-    __device__ __forceinline__ void put(float (&f)[VP]) { v = pack(f), unpack(v, f); }
+    __device__ __forceinline__ void put(float (&f)[VP]) { v = Chunk<T, VP>::from(f), unpack(v, f); }
     __device__ __forceinline__ void get(float (&f)[VP]) const { unpack(v, f); }
 };
 template <typename T, int VP>
@@ -312,7 +324,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
         for (int g = 0; g < G; ++g) {
             float f[4][VP] = {};
             if constexpr (JOIN == kDropped && !RAG) {
-                uint4 x[4] = {}, r[4] = {};
+                typename Chunk<T, VP>::type x[4], r[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     x[j] = now.raw(stage, NT, 0, g, j);  // zeros past the map's end
@@ -587,7 +599,10 @@ template <typename T>
 bool fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     constexpr int V = kVec<T>;
     if (!aligned({a.x, a.residual})) return false;
-    if (m.HW % V == 0 && aligned({a.h}) && (uintptr_t)a.y % (a.q8 >= 0 ? V : 16) == 0) return pick_fwd<T, V, 0>(m, a, d, sms, s);
+    if (aligned({a.h}) && (uintptr_t)a.y % (a.q8 >= 0 ? V : 16) == 0) {
+        if (m.HW % V == 0) return pick_fwd<T, V, 0>(m, a, d, sms, s);
+        if (m.HW % (V / 2) == 0) return pick_fwd<T, V / 2, 0>(m, a, d, sms, s);
+    }
     return pick_fwd<T, kRagged, kRaggedLanes>(m, a, d, sms, s);
 }
 
@@ -607,8 +622,10 @@ template <typename T>
 int bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     constexpr int V = kVec<T>;
     if (!aligned({a.h, a.dy, a.dh})) return 0;
-    if (m.HW % V == 0 && aligned({a.dres, a.dx}))
-        return a.dx ? run_bwd<T, V, 0, true>(m, a, d, sms, s) : run_bwd<T, V, 0, false>(m, a, d, sms, s);
+    if (aligned({a.dres, a.dx})) {
+        if (m.HW % V == 0) return a.dx ? run_bwd<T, V, 0, true>(m, a, d, sms, s) : run_bwd<T, V, 0, false>(m, a, d, sms, s);
+        if (m.HW % (V / 2) == 0) return a.dx ? run_bwd<T, V / 2, 0, true>(m, a, d, sms, s) : run_bwd<T, V / 2, 0, false>(m, a, d, sms, s);
+    }
     return a.dx ? run_bwd<T, kRagged, kRaggedLanes, true>(m, a, d, sms, s) : run_bwd<T, kRagged, kRaggedLanes, false>(m, a, d, sms, s);
 }
 

@@ -54,6 +54,8 @@ template <int VP>
 __device__ __forceinline__ void q8_store(uint8_t* o, const float (&f)[VP], int q8) {
     if constexpr (VP == 1) {
         *o = q8_one(f[0], q8);
+    } else if constexpr (VP == 2) {
+        *reinterpret_cast<uint16_t*>(o) = (uint16_t)q8_pack4(f[0], f[1], 0.0f, 0.0f, q8);
     } else if constexpr (VP == 4) {
         *reinterpret_cast<uint32_t*>(o) = q8_pack4(f[0], f[1], f[2], f[3], q8);
     } else {

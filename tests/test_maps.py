@@ -24,7 +24,7 @@ F32, BF16 = torch.float32, torch.bfloat16
 
 # (B, C, H, W): one element; single rows and pixels; odd, ragged and vector-sized extents; planes that end inside a
 # tile of pixels; channel counts around every way the kernels hold a row, and past them all.
-MAPS = [(1, 1, 1, 1), (1, 3, 1, 1), (2, 1, 5, 7), (3, 5, 7, 7), (2, 8, 4, 4), (1, 17, 3, 11), (2, 96, 8, 8),
+MAPS = [(1, 1, 1, 1), (2, 37, 14, 14), (1, 96, 10, 9), (1, 3, 1, 1), (2, 1, 5, 7), (3, 5, 7, 7), (2, 8, 4, 4), (1, 17, 3, 11), (2, 96, 8, 8),
         (2, 101, 9, 5), (1, 130, 4, 12), (3, 64, 12, 11), (2, 192, 7, 7), (1, 320, 5, 8), (1, 768, 7, 7),
         (1, 1000, 2, 3), (1, 1030, 2, 8), (1, 2050, 1, 9), (1, 4100, 2, 4), (1, 9000, 1, 8), (1, 33000, 1, 2)]
 ROWS = [(1, 1), (1, 7), (5, 8), (33, 96), (300, 100), (1, 768), (7, 1024), (3, 2048), (2, 4096), (2, 8200), (1, 33001)]
@@ -205,7 +205,8 @@ WIDTHS = [2, 4, 9, 16, 31, 32, 33, 40, 63, 64, 65, 96, 127, 128, 129, 192, 255, 
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("layout,hw", [("rows", (1, 1)), ("nchw", (2, 8)), ("nchw", (1, 7)), ("nchw", (3, 43))])
+@pytest.mark.parametrize("layout,hw", [("rows", (1, 1)), ("nchw", (2, 8)), ("nchw", (1, 7)), ("nchw", (3, 43)), ("nchw", (2, 6)),
+                                       ("nchw", (1, 10))])
 def test_every_width(layout, hw, dtype):
     for C in WIDTHS:
         shape = (3 if layout == "rows" else 1, C, *hw)
