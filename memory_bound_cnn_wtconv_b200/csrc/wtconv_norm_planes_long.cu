@@ -12,6 +12,29 @@ namespace {
 
 constexpr int kWarps = 16;
 
+// The sum over all owners of channels for each of the tile's lp pixels, through
+// `finish(pixel, sum)`, which runs once a pixel; every owner gets its result.
+// smem: [kWarps + 1][lp] floats.
+template <typename F>
+__device__ __forceinline__ float lane_sum(float v, int lp, float* smem, F finish) {
+    const int lane = threadIdx.x % 32, pl = lane & (lp - 1);
+    for (int o = lp; o < 32; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane < lp) smem[(threadIdx.x / 32) * lp + pl] = v;
+    __syncthreads();
+    if (threadIdx.x < lp) {
+        float s = smem[threadIdx.x];
+        for (int k = 1; k < kWarps; ++k) s += smem[k * lp + threadIdx.x];
+        smem[kWarps * lp + threadIdx.x] = finish(threadIdx.x, s);
+    }
+    __syncthreads();
+    return smem[kWarps * lp + pl];
+}
+
+// Keep bits of a pixel's quad.
+__device__ __forceinline__ uint32_t keep_pixel(const MapDrop& d, uint32_t offset, long long row, long long b, int quad) {
+    return keep_bits(d, drop_words(d, offset, d.mode == WTCONV_DROP_ELEMENT ? row : b, quad));
+}
+
 template <typename T, int JOIN, bool Q8>
 __global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_kernel(MapShape m, NormFwdArgs a, MapDrop d, int lp, int tiles) {
     extern __shared__ float smem[];  // tile_sum's, then (Q8) the groups' largest bits
@@ -30,11 +53,11 @@ __global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_kernel(Ma
         T* h = static_cast<T*>(a.h) + base;
         bool whole = true;
         if (JOIN == kDropped && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, b);
-        float ss[1] = {};
+        float ss = 0.0f;
         for (int g = 0; g < iters; ++g) {
             const int quad = g * owners + owner;
             uint32_t keep = whole ? 15u : 0u;
-            if (JOIN == kDropped && d.mode != WTCONV_DROP_SAMPLE) keep = keep_tile<1>(d, offset, row, b, quad);
+            if (JOIN == kDropped && d.mode != WTCONV_DROP_SAMPLE) keep = keep_pixel(d, offset, row, b, quad);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = 4 * quad + j;
@@ -49,16 +72,16 @@ __global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_kernel(Ma
                     h[at] = v;
                     f = to_f(v);  // the norm is of h as it is stored
                 }
-                ss[0] += f * f;
+                ss += f * f;
             }
         }
-        lane_tile_sum<1>(ss, lp, smem, [&](int q, float s) {
+        ss = lane_sum(ss, lp, smem, [&](int q, float s) {
             const float r = rsqrtf(s / m.C + a.eps);
             if (a.rstd && p0 + q < m.HW) a.rstd[b * m.HW + p0 + q] = r;
             return r;
         });
         const T* hs = JOIN == kPlain ? x : h;  // what this thread wrote itself
-        auto value = [&](int c) { return to_f(hs[(long long)c * m.HW]) * ss[0] * a.weight[c]; };
+        auto value = [&](int c) { return to_f(hs[(long long)c * m.HW]) * ss * a.weight[c]; };
         if (!Q8) {
             for (int g = 0; g < iters; ++g) {
 #pragma unroll
@@ -125,20 +148,20 @@ __global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_bwd_kerne
         bool whole = true;
         if (DROP && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, b);
         const float r = live ? a.rstd[row] : 0.0f;
-        float gh[1] = {};
+        float gh = 0.0f;
         for (int g = 0; g < iters; ++g) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = 4 * (g * owners + owner) + j;
-                if (live && c < m.C) gh[0] += to_f(dy[(long long)c * m.HW]) * to_f(h[(long long)c * m.HW]) * a.weight[c];
+                if (live && c < m.C) gh += to_f(dy[(long long)c * m.HW]) * to_f(h[(long long)c * m.HW]) * a.weight[c];
             }
         }
-        lane_tile_sum<1>(gh, lp, smem, [&](int, float s) { return s / m.C; });
-        const float s = gh[0] * r * r;
+        gh = lane_sum(gh, lp, smem, [&](int, float s) { return s / m.C; });
+        const float s = gh * r * r;
         for (int g = 0; g < iters; ++g) {
             const int quad = g * owners + owner;
             uint32_t keep = whole ? 15u : 0u;
-            if (DROP && d.mode != WTCONV_DROP_SAMPLE) keep = keep_tile<1>(d, offset, row, b, quad);
+            if (DROP && d.mode != WTCONV_DROP_SAMPLE) keep = keep_pixel(d, offset, row, b, quad);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = 4 * quad + j;
