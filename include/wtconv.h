@@ -234,9 +234,9 @@ wtconv_status_t wtconv_backward_weight_noalloc(const wtconv_desc_t *d, const voi
  *   - Any B >= 0 (0: nothing to do, dweight is zeroed), C, H, W > 0; no
  *     multiple is asked for.  Offsets are 64-bit.  H*W <= 2^30, C <= 2^24.
  *   - Activations are contiguous, in desc->dtype; they are aligned to their
- *     element.  (Where the pointers are 16-byte aligned and the adjacent
- *     extent, C for NHWC and H*W for NCHW, is whole 16-byte chunks, the
- *     kernels use 16-byte accesses.)
+ *     element.  (The kernels use 16-byte accesses where the pointers are
+ *     16-byte aligned and the adjacent extent, C for NHWC and H*W for NCHW, is
+ *     whole 16-byte chunks; 8-byte ones for NCHW where it is whole halves.)
  *   - Outputs overlap neither an input nor another output (WTCONV_ERR_ARGUMENT).
  *   - Results do not depend on the order in which CTAs run: repeated calls
  *     return the same bits.

@@ -623,9 +623,11 @@ def test_modules():
     assert torch.equal(y, wt.rms_norm_forward(h, norm.weight.detach())[0])
 
 
-def test_offsets_past_32_bits():
-    # Rows and elements past 2^31: the last pixels of a map of 2^31 + some elements, in both layouts.
-    B, C, H, W = 1, 8, 16400, 16400
+@pytest.mark.parametrize("B,side", [(1, 16400), (3, 10400)])
+def test_offsets_past_31_bits(B, side):
+    # The last pixels of maps of over 2^31 elements, in one sample or in several, in both layouts.
+    C = 8
+    H = W = side
     x = torch.zeros(B, C, H, W, dtype=BF16, device="cuda")
     tail = torch.randn(1, C, 1, 64, generator=gen_of("far")).to(BF16).cuda()
     w = torch.rand(C, generator=gen_of("far")).cuda() + 0.5
@@ -633,20 +635,41 @@ def test_offsets_past_32_bits():
     for cl in (False, True):
         if cl:
             x = x.contiguous(memory_format=torch.channels_last)
-        x[:, :, -1:, -64:] = tail
+        x[-1:, :, -1:, -64:] = tail
         y, _, rstd = wt.rms_norm_forward(x, w, eps=EPS)
-        part = y[:, :, -1:, -64:].contiguous()
-        check_forward(tail, None, w, None, part, tail, rstd[:, -1:, -64:].contiguous())
-        assert not y[:, :, -1, :-64].any() and not y[:, :, 0].any()
+        part = y[-1:, :, -1:, -64:].contiguous()
+        check_forward(tail, None, w, None, part, tail, rstd[-1:, -1:, -64:].contiguous())
+        assert not y[-1, :, -1, :-64].any() and not y[:, :, 0].any()
         dx, _, dw = wt.rms_norm_backward(x, y, w, rstd)
-        t2, _, r2 = wt.rms_norm_forward(tail, w, eps=EPS)
-        check_backward(tail, part, None, w, None, dx[:, :, -1:, -64:].contiguous(), dx[:, :, -1:, -64:].contiguous(), None)
-        size = (wide(part) * wide(tail) / np.sqrt((wide(tail) ** 2).mean(1, keepdims=True) + EPS)).sum((0, 2))
-        close(dw.double().cpu().numpy(), size, 1e-4 * np.abs(size) + 1e-5, "dweight")
+        last = dx[-1:, :, -1:, -64:].contiguous()
+        check_backward(tail, part, None, w, None, last, last, None)
+        assert not dx[:, :, 0].any()
+        # the zeros add nothing: the sum of the last 64 rows, whatever shares of the rows the CTAs add up
+        t = wide(tail)
+        terms = wide(part) * t / np.sqrt((t ** 2).mean(1, keepdims=True) + EPS)
+        close(dw.double().cpu().numpy(), terms.sum((0, 2)), (64 + C / 2 + 14) * U * np.abs(terms).sum((0, 2)), "dweight")
+        del dx, y
         y = wt.dropout_forward(x, drop)
-        row = np.arange(H * W - 64, H * W, dtype=np.uint64)
+        row = np.arange(B * H * W - 64, B * H * W, dtype=np.uint64)
         words = [ref.philox4x32((np.full(64, q, np.uint64), row, row >> np.uint64(32), np.zeros(64, np.uint64)), (13, 0))
                  for q in range(2)]
         keep = np.stack([u for ws in words for u in ws]) >= np.uint64(1 << 31)
-        assert np.array_equal(wide(y[:, :, -1:, -64:])[0], np.where(keep, wide(tail)[0] * 2.0, 0.0))
-        del y, dx
+        assert np.array_equal(wide(y[-1:, :, -1:, -64:])[0], np.where(keep, wide(tail)[0] * 2.0, 0.0))
+        q, scale, _ = wt.rms_norm_q8(x, w, group=32)
+        v, _ = ref.norm(t, w.double().cpu().numpy(), 1e-6)
+        s8 = wide(scale[-1:, :, -1:, -64:])
+        close(wide(q[-1:, :, -1:, -64:].float()) * s8, v, np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -10 * s8) * 1.001 + 1e-5 * np.abs(v), "q")
+        del y, q, scale
+
+
+def test_rows_past_32_bits():
+    # The counter's second word: mask rows over 2^32.
+    B, side = 5, 1 << 15
+    x = torch.ones(B, 1, side, side, dtype=BF16, device="cuda")
+    y = wt.dropout_forward(x, wt.Drop(0.5, "element", 17, 3))
+    for first in (0, (1 << 32) - 32, B * side * side - 64):
+        row = np.arange(first, first + 64, dtype=np.uint64)
+        word = ref.philox4x32((np.zeros(64, np.uint64), row & np.uint64(0xFFFFFFFF), row >> np.uint64(32),
+                               np.full(64, 3, np.uint64)), (17, 0))[0]
+        got = y.view(-1)[first:first + 64].double().cpu().numpy()
+        assert np.array_equal(got, np.where(word >= np.uint64(1 << 31), 2.0, 0.0))
