@@ -98,47 +98,50 @@ def _lib():
     return _fns
 
 
-def _desc(x: torch.Tensor, name: str) -> MapDesc:
+class _Map:
+    """What a call needs to know of the shape, type and layout of its activations."""
+
+    __slots__ = ("desc", "ref", "C", "layout", "flat", "rows")
+
+    def __init__(self, shape, dtype, layout: int):
+        B, C, H, W = shape if len(shape) == 4 else (*shape, 1, 1)
+        self.desc = MapDesc(B, C, H, W, F32 if dtype is torch.float32 else BF16, layout)
+        self.ref = ctypes.byref(self.desc)
+        self.C, self.layout = C, layout
+        self.flat = layout == NCHW or len(shape) == 2  # contiguous, not channels-last
+        self.rows = (B,) if len(shape) == 2 else (B, H, W)
+
+
+_maps = {}  # by shape, type and layout
+
+
+def _map_of(x: torch.Tensor, name: str) -> _Map:
     """The map that a tensor is; raises for what is none."""
-    if x.dtype is torch.float32:
-        dtype = F32
-    elif x.dtype is torch.bfloat16:
-        dtype = BF16
-    else:
+    key = (x.shape, x.dtype, x.is_contiguous())
+    if x.is_cuda and (m := _maps.get(key)) is not None and (key[2] or x.is_contiguous(memory_format=torch.channels_last)):
+        return m
+    if x.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"activations must be float32 or bfloat16, got {x.dtype}")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    shape = x.shape
-    if len(shape) == 4:
-        if x.is_contiguous():
-            layout = NCHW
-        elif x.is_contiguous(memory_format=torch.channels_last):
-            layout = NHWC
-        else:
-            raise ValueError(f"{name} must be contiguous (NCHW) or channels-last contiguous (NHWC)")
-        B, C, H, W = shape
-        if H == 0 or W == 0:
-            raise ValueError(f"{name} has no pixels: {tuple(shape)}")
-    elif len(shape) == 2:
-        if not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        B, C = shape
-        H = W = 1
-        layout = NHWC
-    else:
-        raise ValueError(f"{name} must be a [B, C, H, W] map or [N, C] rows, got {len(shape)} dimensions")
-    if C == 0:
-        raise ValueError(f"{name} has no channels: {tuple(shape)}")
-    return MapDesc(B, C, H, W, dtype, layout)
+    if x.dim() not in (2, 4):
+        raise ValueError(f"{name} must be a [B, C, H, W] map or [N, C] rows, got {x.dim()} dimensions")
+    if not key[2] and not (x.dim() == 4 and x.is_contiguous(memory_format=torch.channels_last)):
+        raise ValueError(f"{name} must be contiguous (NCHW, rows) or channels-last contiguous (NHWC)")
+    if 0 in x.shape[1:]:
+        raise ValueError(f"{name} has no channels or no pixels: {tuple(x.shape)}")
+    if len(_maps) >= 4096:
+        _maps.clear()
+    _maps[key] = m = _Map(tuple(x.shape), x.dtype, NCHW if key[2] and x.dim() == 4 else NHWC)
+    return m
 
 
-def _like(t: torch.Tensor, name: str, x: torch.Tensor, layout: int, dtype=None) -> int:
+def _like(t: torch.Tensor, name: str, x: torch.Tensor, m: _Map, dtype=None) -> int:
     """The address of an activation that has to be as x is."""
     if t.dtype is not (dtype or x.dtype) or t.shape != x.shape or t.get_device() != x.get_device():
         raise ValueError(f"{name} must have the shape {tuple(x.shape)}, type {dtype or x.dtype} and device of the input")
-    if not t.is_contiguous(memory_format=torch.channels_last if layout == NHWC and t.dim() == 4
-                           else torch.contiguous_format):
-        raise ValueError(f"{name} must have the layout of the input ({'NHWC' if layout == NHWC else 'NCHW'})")
+    if not (t.is_contiguous() if m.flat else t.is_contiguous(memory_format=torch.channels_last)):
+        raise ValueError(f"{name} must have the layout of the input ({'NHWC' if m.layout == NHWC else 'NCHW'})")
     return t.data_ptr()
 
 
@@ -156,11 +159,6 @@ def _drop_ref(drop, x):
     if drop._args.offset_dev is not None and drop.offset.device != x.device:
         raise ValueError(f"the offset tensor is on {drop.offset.device}, the activations on {x.device}")
     return ctypes.byref(drop._args)
-
-
-def _rows_shape(x: torch.Tensor):
-    s = x.shape
-    return s[:1] if len(s) == 2 else (s[0], s[2], s[3])
 
 
 def _elsewhere(x, stream) -> bool:
@@ -184,18 +182,18 @@ def _stream_of(x) -> int:
 def dropout_forward(x, drop: Drop, residual=None, y=None, stream=None):
     """y = residual + drop(x) via ``wtconv_dropout``; returns y (allocated if
     not given)."""
-    d = _desc(x, "x")
+    m = _map_of(x, "x")
     if _elsewhere(x, stream):
         with _there(x, stream):
             return dropout_forward(x, drop, residual, y)
     ref = _drop_ref(drop, x)
-    rp = None if residual is None else _like(residual, "residual", x, d.layout)
+    rp = None if residual is None else _like(residual, "residual", x, m)
     if y is None:
         y = torch.empty_like(x)
         yp = y.data_ptr()
     else:
-        yp = _like(y, "y", x, d.layout)
-    _check(_lib().wtconv_dropout(ctypes.byref(d), ref, x.data_ptr(), rp, yp, _stream_of(x)), "wtconv_dropout")
+        yp = _like(y, "y", x, m)
+    _check(_lib().wtconv_dropout(m.ref, ref, x.data_ptr(), rp, yp, _stream_of(x)), "wtconv_dropout")
     return y
 
 
@@ -210,47 +208,47 @@ def rms_norm_forward(x, weight, residual=None, drop: Drop = None, eps: float = 1
     """h = residual + drop(x), y = h / rms(h) * weight via
     ``wtconv_rms_norm_forward``; returns (y, h, rstd).  Without a residual h is
     x itself.  ``rstd=False`` leaves rstd out (inference): None is returned."""
-    d = _desc(x, "x")
+    m = _map_of(x, "x")
     if _elsewhere(x, stream):
         with _there(x, stream):
             return rms_norm_forward(x, weight, residual, drop, eps, y, h, rstd)
-    wp = _vector(weight, "weight", x, (d.C,))
+    wp = _vector(weight, "weight", x, (m.C,))
     ref = None if drop is None else _drop_ref(drop, x)
     if residual is None:
         if h is not None:
             raise ValueError("without a residual, h is x: give none")
         h, rp, hp = x, None, None
     else:
-        rp = _like(residual, "residual", x, d.layout)
+        rp = _like(residual, "residual", x, m)
         if h is None:
             h = torch.empty_like(x)
             hp = h.data_ptr()
         else:
-            hp = _like(h, "h", x, d.layout)
+            hp = _like(h, "h", x, m)
     if y is None:
         y = torch.empty_like(x)
         yp = y.data_ptr()
     else:
-        yp = _like(y, "y", x, d.layout)
+        yp = _like(y, "y", x, m)
     if rstd is None:
-        rstd = weight.new_empty(_rows_shape(x))
+        rstd = weight.new_empty(m.rows)
         sp = rstd.data_ptr()
     elif rstd is False:
         rstd = sp = None
     else:
-        sp = _vector(rstd, "rstd", x, _rows_shape(x))
-    _check(_lib().wtconv_rms_norm_forward(ctypes.byref(d), eps, x.data_ptr(), rp, ref, wp, yp, hp, sp, _stream_of(x)),
+        sp = _vector(rstd, "rstd", x, m.rows)
+    _check(_lib().wtconv_rms_norm_forward(m.ref, eps, x.data_ptr(), rp, ref, wp, yp, hp, sp, _stream_of(x)),
            "wtconv_rms_norm_forward")
     return y, h, rstd
 
 
 def rms_norm_workspace_bytes(x: torch.Tensor) -> int:
     """Workspace of ``rms_norm_backward`` for activations like x."""
-    d = _desc(x, "x")
+    m = _map_of(x, "x")
     if _elsewhere(x, None):
         with _there(x, None):
             return rms_norm_workspace_bytes(x)
-    return _lib().wtconv_rms_norm_workspace_bytes(ctypes.byref(d))
+    return _lib().wtconv_rms_norm_workspace_bytes(m.ref)
 
 
 def rms_norm_backward(h, dy, weight, rstd, dh=None, drop: Drop = None, dx=None, dresidual=None, dweight=None,
@@ -262,15 +260,14 @@ def rms_norm_backward(h, dy, weight, rstd, dh=None, drop: Drop = None, dx=None, 
     given as False is left out (None is returned; without ``drop`` False for
     either of the two stands for both).  ``workspace`` is a CUDA tensor of at
     least ``rms_norm_workspace_bytes`` bytes; allocated here if not given."""
-    d = _desc(h, "h")
+    m = _map_of(h, "h")
     if _elsewhere(h, stream):
         with _there(h, stream):
             return rms_norm_backward(h, dy, weight, rstd, dh, drop, dx, dresidual, dweight, workspace)
-    layout = d.layout
-    dyp = _like(dy, "dy", h, layout)
-    wp = _vector(weight, "weight", h, (d.C,))
-    rsp = _vector(rstd, "rstd", h, _rows_shape(h))
-    dhp = None if dh is None else _like(dh, "dh", h, layout)
+    dyp = _like(dy, "dy", h, m)
+    wp = _vector(weight, "weight", h, (m.C,))
+    rsp = _vector(rstd, "rstd", h, m.rows)
+    dhp = None if dh is None else _like(dh, "dh", h, m)
     gp = ref = None
     if drop is None:
         if dx is False or dresidual is False:
@@ -287,14 +284,14 @@ def rms_norm_backward(h, dy, weight, rstd, dh=None, drop: Drop = None, dx=None, 
         elif dx is False:
             dx = None
         else:
-            gp = _like(dx, "dx", h, layout)
+            gp = _like(dx, "dx", h, m)
     if dresidual is None:
         dresidual = torch.empty_like(h)
         rp = dresidual.data_ptr()
     elif dresidual is False:
         dresidual = rp = None
     else:
-        rp = _like(dresidual, "dresidual", h, layout)
+        rp = _like(dresidual, "dresidual", h, m)
     if drop is None:
         dx = dresidual
     lib = _lib()
@@ -309,16 +306,16 @@ def rms_norm_backward(h, dy, weight, rstd, dh=None, drop: Drop = None, dx=None, 
             dweight = torch.empty_like(weight)
             dwp = dweight.data_ptr()
         else:
-            dwp = _vector(dweight, "dweight", h, (d.C,))
+            dwp = _vector(dweight, "dweight", h, (m.C,))
         if workspace is None:
-            nbytes = lib.wtconv_rms_norm_workspace_bytes(ctypes.byref(d))
+            nbytes = lib.wtconv_rms_norm_workspace_bytes(m.ref)
             workspace = weight.new_empty(((nbytes + 3) // 4,))
             wsp = workspace.data_ptr()
         else:
             if not workspace.is_cuda or workspace.device != h.device or not workspace.is_contiguous():
                 raise ValueError(f"workspace must be a contiguous tensor on {h.device}")
             wsp, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib.wtconv_rms_norm_backward(ctypes.byref(d), h.data_ptr(), dyp, dhp, ref, wp, rsp, rp, gp, dwp, wsp, nbytes,
+    _check(lib.wtconv_rms_norm_backward(m.ref, h.data_ptr(), dyp, dhp, ref, wp, rsp, rp, gp, dwp, wsp, nbytes,
                                         _stream_of(h)), "wtconv_rms_norm_backward")
     return dx, dresidual, dweight
 
@@ -334,31 +331,30 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, dtype=torch.float8_
         raise TypeError(f"dtype must be torch.float8_e4m3fn or torch.int8, got {dtype}")
     if group not in (0, 32, 64, 128):
         raise ValueError(f"group must be 0, 32, 64 or 128, got {group}")
-    d = _desc(x, "x")
+    m = _map_of(x, "x")
     if _elsewhere(x, stream):
         with _there(x, stream):
             return rms_norm_q8(x, weight, residual, eps, dtype, group, q, scale, h)
-    layout = d.layout
-    wp = _vector(weight, "weight", x, (d.C,))
+    wp = _vector(weight, "weight", x, (m.C,))
     if residual is None:
         if h is not None:
             raise ValueError("without a residual, h is x: give none")
         h, rp, hp = x, None, None
     else:
-        rp = _like(residual, "residual", x, layout)
+        rp = _like(residual, "residual", x, m)
         if h is None:
             h = torch.empty_like(x)
             hp = h.data_ptr()
         else:
-            hp = _like(h, "h", x, layout)
+            hp = _like(h, "h", x, m)
     if q is None:
         q = torch.empty_like(x, dtype=dtype)
         qp = q.data_ptr()
     else:
-        qp = _like(q, "q", x, layout, dtype)
-    groups = -(-d.C // group) if group else 1
+        qp = _like(q, "q", x, m, dtype)
+    groups = -(-m.C // group) if group else 1
     shape = (x.shape[0], groups, *x.shape[2:])
-    nhwc = layout == NHWC and x.dim() == 4
+    nhwc = not m.flat
     if scale is None:
         scale = weight.new_empty((shape[0], *shape[2:], groups) if nhwc else shape)
         if nhwc:
@@ -366,7 +362,7 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, dtype=torch.float8_
     elif scale.dtype is not torch.float32 or scale.shape != shape or scale.device != x.device \
             or not scale.is_contiguous(memory_format=torch.channels_last if nhwc else torch.contiguous_format):
         raise ValueError(f"scale must be a float32 tensor of shape {shape} in the layout of x on {x.device}")
-    _check(_lib().wtconv_rms_norm_q8(ctypes.byref(d), eps, x.data_ptr(), rp, wp, _Q8[dtype], group, qp,
+    _check(_lib().wtconv_rms_norm_q8(m.ref, eps, x.data_ptr(), rp, wp, _Q8[dtype], group, qp,
                                      scale.data_ptr(), hp, _stream_of(x)), "wtconv_rms_norm_q8")
     return q, scale, h
 
