@@ -1,8 +1,7 @@
 // Shared parts of the map operators (RMS norm over channels, dropout): the
 // shape they run on, stored-type conversions, and the counter-based mask.
 //
-// A map is B x C x H x W.  Its rows are the B*H*W pixels, n = b*H*W + p; the
-// C values of a row are `cs` elements apart (NHWC: 1, NCHW: H*W).
+// A map is B x C x H x W.  Its rows are the B*H*W pixels, n = b*H*W + p.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -180,6 +179,7 @@ __device__ __forceinline__ void drop_add4(const MapDrop& d, const uint4& u, cons
     if (u.z >= d.thresh) r[2] = __fmaf_rn(f[2], d.grown, r[2]);
     if (u.w >= d.thresh) r[3] = __fmaf_rn(f[3], d.grown, r[3]);
 }
+
 // T(r + d * x) of a chunk (or half a one) of pixels of four channels, into r, word
 // by word, so that few values are held as floats at once.
 template <typename T>
@@ -214,14 +214,12 @@ __device__ __forceinline__ void drop_add_chunks(const MapDrop& d, uint32_t offse
             for (int v = 0; v < N; ++v) u[v] = drop_words(d, offset, lo + k * N + v, hi, quad);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            drop_add_words<T>(d, u, word_of(x[j], k), word_of(r[j], k), j);
-        }
+        for (int j = 0; j < 4; ++j) drop_add_words<T>(d, u, word_of(x[j], k), word_of(r[j], k), j);
     }
 }
 
-// r + d * f of N pixels of four channels, into r; lo: the first pixel's row,
-// a multiple of N; b: the sample.
+// r + d * f of N pixels of four channels, into r; row: the first pixel's (all of
+// them share its upper word); b: the sample.
 template <int N>
 __device__ __forceinline__ void drop_add_tile(const MapDrop& d, uint32_t offset, long long row, long long b, int quad,
                                               const float (&f)[4][N], float (&r)[4][N]) {

@@ -62,9 +62,11 @@ struct PlanesGeom {
     float per_channel;             // 1 / C
 };
 
-// Tiles of 128 bytes of a plane (64 pixels where it is ragged), less where two stages of `tensors` tensors do not
-// leave room for two CTAs on an SM, down to 64 bytes, and then what fits at
-// all.  False if nothing does.
+// Tiles of 128 bytes of a plane (64 pixels where it is ragged), less where two
+// stages of `tensors` tensors do not leave room for two CTAs on an SM, down to
+// 64 bytes, and then what fits at all (wider tiles weigh more than a second
+// CTA there: 768 ragged channels, 128 x 7 x 7 bf16, 43 us at 32 bytes, 59 at 16).
+// False if nothing does.
 inline bool planes_geom(const MapShape& m, int VP, bool ragged, int esize, int tensors, PlanesGeom* out) {
     if ((long long)m.C * m.HW >= 1LL << 31) return false;  // offsets within a sample are 32-bit
     const int quads = (m.C + 3) / 4;
@@ -76,8 +78,7 @@ inline bool planes_geom(const MapShape& m, int VP, bool ragged, int esize, int t
         const int lanes = 32 / lp;
         g.lp = lp;
         // Two quads an owner where one needs too many warps (ragged: where that leaves four, for less work around a tile).
-        g.iters = ragged && quads >= 2 * 4 * lanes ? 2 : 1;
-        while (g.iters < 2 && (quads + lanes * g.iters - 1) / (lanes * g.iters) > kMaxWarps) g.iters *= 2;
+        g.iters = (ragged && quads >= 2 * 4 * lanes) || (quads + lanes - 1) / lanes > kMaxWarps ? 2 : 1;
         g.warps = (quads + lanes * g.iters - 1) / (lanes * g.iters);
         if (g.warps > kMaxWarps) continue;
         g.owners = g.warps * lanes;

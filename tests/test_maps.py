@@ -525,6 +525,18 @@ def test_autograd_forms():
         xl.grad = rl.grad = None
         wt.dropout(xl, drop, rl).backward(dy)
         assert torch.equal(xl.grad, wt.dropout_backward(dy, drop)) and torch.equal(rl.grad, dy)
+    # one tensor as both branch and residual; the two leaves' gradients are tensors of their own
+    both = x.clone().requires_grad_()
+    y, h = wt.rms_norm(both, w.detach(), both)
+    torch.autograd.backward([y, h], [dy, dh])
+    y2, h2, rstd = wt.rms_norm_forward(x, w.detach(), x)
+    d = wt.rms_norm_backward(h2, dy, w.detach(), rstd, dh)[0]
+    assert torch.equal(both.grad, d + d)
+    xl, rl = x.clone().requires_grad_(), res.clone().requires_grad_()
+    wt.rms_norm(xl, w.detach(), rl)[0].backward(dy)
+    kept = rl.grad.clone()
+    xl.grad.zero_()
+    assert torch.equal(rl.grad, kept)
     # strided activations are laid out first; gradients arrive in any layout
     t = torch.randn(2, 6, 20, 5, device="cuda").transpose(1, 2).requires_grad_()
     g = torch.randn(2, 5, 6, 20, device="cuda").permute(0, 3, 2, 1)
