@@ -9,32 +9,9 @@
 #include <stdint.h>
 
 #include "../../include/wtconv.h"
-#include "wtconv_plan.h"
+#include "wtconv_map_geom.h"
 
 namespace wtc {
-
-struct MapShape {
-    long long rows;  // B * H * W
-    int C, HW;
-    int nhwc;        // 1: the C values of a row are adjacent
-};
-
-// n / d of a count: a multiply and a shift below 2^31, else a division.
-struct Divide {
-    FastDiv f;
-    long long d;
-    int small;  // every n is below 2^31
-    __device__ __forceinline__ long long operator()(long long n) const {
-        return small ? (long long)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift) : n / d;
-    }
-};
-inline Divide divide_by(long long d, long long most) {
-    Divide v{};
-    v.d = d;
-    v.small = most < (1LL << 31) && d < (1LL << 31);
-    if (v.small) v.f = make_fastdiv((uint32_t)d);
-    return v;
-}
 
 // Dropout of one call.  Nothing is dropped when `on` is 0.
 struct MapDrop {

@@ -9,13 +9,6 @@
 
 namespace wtc {
 
-// CTAs of the backward whose partial sums of the weight gradient the workspace
-// holds, one vector of C floats for each: eight for every SM, fewer where that
-// is over 32 MB, but 64.
-inline long long norm_parts(const MapShape& m, int sms) {
-    return std::min(m.rows, std::max(64LL, std::min(8LL * sms, (1LL << 23) / m.C)));
-}
-
 // CTAs of a kernel that an SM holds.
 template <typename K>
 int norm_resident(K kernel, int threads, size_t smem) {

@@ -188,8 +188,8 @@ bool run_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms,
     PlanesGeom g;
     if (!planes_geom(m, VP, RAG, sizeof(T), JOIN == kPlain ? 1 : 2, &g)) return false;
     const int groups = Q8 ? (m.C + a.group - 1) / a.group : 0;
-    const size_t smem = g.head + (size_t)(g.warps + 1 + groups) * g.lp * VP * 4;
-    if (smem > 225 * 1024) return false;
+    const size_t smem = g.head + (size_t)planes_sums(g, VP, groups) * 4;
+    if (smem > kMostSmem) return false;
     planes_dispatch<RAG>(g, [&](auto rag, auto quads) {
         return launch(wtconv_norm_planes_kernel<T, VP, rag, quads, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
     });

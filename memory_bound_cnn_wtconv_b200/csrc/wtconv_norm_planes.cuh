@@ -44,60 +44,6 @@ __device__ __forceinline__ void q8_store(uint8_t* o, const float (&f)[VP], int q
     }
 }
 
-constexpr int kMaxWarps = 16;
-constexpr int kSmem = 200 * 1024;      // of the 227 KB a CTA may have
-constexpr int kSmemTwo = 104 * 1024;   // two CTAs an SM, with their sums
-
-constexpr int kRagged = 4;       // pixels of a thread where planes are ragged
-constexpr int kRaggedLanes = 16;  // lanes along them, at compile time (constant offsets), unless that does not fit
-
-struct PlanesGeom {
-    int lp, warps, owners, iters;  // iters: quads of an owner
-    int tiles;                     // of a plane
-    int row;                       // ragged: bytes of a channel's pixels in a stage
-    int tensor;                    // bytes of one tensor in a stage
-    int head;                      // bytes of both stages
-    FastDiv by_chunks;             // ragged: row / 16
-    Divide by_tiles;
-    float per_channel;             // 1 / C
-};
-
-// Tiles of 128 bytes of a plane (64 pixels where it is ragged), less where two
-// stages of `tensors` tensors do not leave room for two CTAs on an SM, down to
-// 64 bytes, and then what fits at all (wider tiles weigh more than a second
-// CTA there: 768 ragged channels, 128 x 7 x 7 bf16, 43 us at 32 bytes, 59 at 16).
-// False if nothing does.
-inline bool planes_geom(const MapShape& m, int VP, bool ragged, int esize, int tensors, PlanesGeom* out) {
-    if ((long long)m.C * m.HW >= 1LL << 31) return false;  // offsets within a sample are 32-bit
-    const int quads = (m.C + 3) / 4;
-    int lp = ragged ? kRaggedLanes : 128 / (VP * esize);
-    while (!ragged && lp < 32 && quads * lp <= 16) lp *= 2;
-    while (lp > 1 && lp / 2 * VP >= m.HW) lp /= 2;
-    for (; lp >= 1; lp /= 2) {
-        PlanesGeom g{};
-        const int lanes = 32 / lp;
-        g.lp = lp;
-        // Two quads an owner where one needs too many warps (ragged: where that leaves four, for less work around a tile).
-        g.iters = (ragged && quads >= 2 * 4 * lanes) || (quads + lanes - 1) / lanes > kMaxWarps ? 2 : 1;
-        g.warps = (quads + lanes * g.iters - 1) / (lanes * g.iters);
-        if (g.warps > kMaxWarps) continue;
-        g.owners = g.warps * lanes;
-        g.tiles = (m.HW + lp * VP - 1) / (lp * VP);
-        g.row = (lp * VP * esize + 15) / 16 * 16 + 16;
-        const long long tensor = ragged ? (long long)g.row * m.C : 4LL * VP * esize * g.iters * g.warps * 32;
-        if (2 * tensors * tensor > kSmem) continue;
-        if (2 * tensors * tensor + (g.warps + 1) * lp * VP * 4 > kSmemTwo && lp * VP * esize > 64) continue;
-        g.tensor = (int)tensor;
-        g.head = (int)(2 * tensors * tensor);
-        g.by_chunks = make_fastdiv(g.row / 16);
-        g.by_tiles = divide_by(g.tiles, m.rows);
-        g.per_channel = 1.0f / m.C;
-        *out = g;
-        return true;
-    }
-    return false;
-}
-
 __device__ __forceinline__ void copy16(void* to, const void* from, int bytes) {  // the rest of the 16 bytes as zeros
     const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(to));
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(from), "r"(bytes) : "memory");

@@ -127,7 +127,7 @@ int run_bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, 
         if (!planes_geom(m, VP, RAG, sizeof(T), 2, &g)) return 0;
         dh = !a.dh ? kNone : kDirect;
     }
-    const size_t smem = g.head + (size_t)(g.warps + 1) * g.lp * VP * 4;
+    const size_t smem = g.head + (size_t)planes_sums(g, VP, 0) * 4;
     const long long most = norm_parts(m, sms);
     return planes_dispatch<RAG>(g, [&](auto rag, auto quads) {
         if (dh == kNone) return launch(wtconv_norm_planes_bwd_kernel<T, VP, rag, quads, DROP, kNone>, m, a, d, g, smem, most, sms, s);

@@ -10,7 +10,7 @@ namespace wtc {
 
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = kLongWarps;
 
 // The sum over all owners of channels for each of the tile's lp pixels, through
 // `finish(pixel, sum)`, which runs once a pixel; every owner gets its result.
@@ -36,7 +36,8 @@ __device__ __forceinline__ uint32_t keep_pixel(const MapDrop& d, uint32_t offset
 }
 
 template <typename T, int JOIN, bool Q8>
-__global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_kernel(MapShape m, NormFwdArgs a, MapDrop d, int lp, int tiles) {
+__global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_kernel(MapShape m, NormFwdArgs a, MapDrop d, LongGeom geom) {
+    const int lp = geom.lp, tiles = geom.tiles;
     extern __shared__ float smem[];  // tile_sum's, then (Q8) the groups' largest bits
     const int lane = threadIdx.x % 32, lanes = 32 / lp, owners = kWarps * lanes;
     const int pl = lane & (lp - 1), owner = (threadIdx.x / 32) * lanes + lane / lp;
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_kernel(Ma
         }
         // Rounds of whole groups (a round is 4 * owners channels, a multiple of 128), or the whole row as one.
         uint32_t* top = reinterpret_cast<uint32_t*>(smem + (kWarps + 1) * lp);
-        const int groups = (m.C + a.group - 1) / a.group, n = groups == 1 ? 1 : 4 * owners / a.group;
+        const int groups = (m.C + a.group - 1) / a.group, n = geom.round;
         const int span = groups == 1 ? iters : 1;
         for (int g0 = 0; g0 < iters; g0 += span) {
             const int first = groups == 1 ? 0 : g0 * n;
@@ -131,7 +132,8 @@ __global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_kernel(Ma
 }
 
 template <typename T, bool DROP>
-__global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_bwd_kernel(MapShape m, NormBwdArgs a, MapDrop d, int lp, int tiles) {
+__global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_bwd_kernel(MapShape m, NormBwdArgs a, MapDrop d, LongGeom geom) {
+    const int lp = geom.lp, tiles = geom.tiles;
     extern __shared__ float smem[];
     const int lane = threadIdx.x % 32, lanes = 32 / lp, owners = kWarps * lanes;
     const int pl = lane & (lp - 1), owner = (threadIdx.x / 32) * lanes + lane / lp;
@@ -176,20 +178,12 @@ __global__ void __launch_bounds__(kWarps * 32) wtconv_norm_planes_long_bwd_kerne
     }
 }
 
-// Pixel lanes: all, unless there are few pixels to share out (the weight
-// gradient's sums are taken apart, by columns).
-int lanes_of(const MapShape& m, int sms) {
-    int lp = 32;
-    while (lp > 4 && (lp / 2 >= m.HW || m.rows / lp < sms)) lp /= 2;
-    return lp;
-}
-
 template <typename T, int JOIN, bool Q8>
 void run_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
-    const int lp = lanes_of(m, sms), tiles = (m.HW + lp - 1) / lp;
-    const unsigned grid = (unsigned)std::min(m.rows / m.HW * tiles, 64LL * sms);
-    const int n = !Q8 ? 0 : a.group >= m.C ? 1 : 4 * kWarps * (32 / lp) / a.group;
-    wtconv_norm_planes_long_kernel<T, JOIN, Q8><<<grid, kWarps * 32, (size_t)(kWarps + 1 + n) * lp * 4, s>>>(m, a, d, lp, tiles);
+    const LongGeom g = long_geom(m, sms, Q8, a.group);
+    const unsigned grid = (unsigned)std::min(m.rows / m.HW * g.tiles, 64LL * sms);
+    const size_t smem = (size_t)(kWarps + 1 + g.round) * g.lp * 4;
+    wtconv_norm_planes_long_kernel<T, JOIN, Q8><<<grid, kWarps * 32, smem, s>>>(m, a, d, g);
 }
 
 template <typename T>
@@ -202,11 +196,11 @@ void fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cud
 
 template <typename T>
 void bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
-    const int lp = lanes_of(m, sms), tiles = (m.HW + lp - 1) / lp;
-    const unsigned grid = (unsigned)std::min(m.rows / m.HW * tiles, 64LL * sms);
-    const size_t smem = (size_t)(kWarps + 1) * lp * 4;
-    if (a.dx) wtconv_norm_planes_long_bwd_kernel<T, true><<<grid, kWarps * 32, smem, s>>>(m, a, d, lp, tiles);
-    else wtconv_norm_planes_long_bwd_kernel<T, false><<<grid, kWarps * 32, smem, s>>>(m, a, d, lp, tiles);
+    const LongGeom g = long_geom(m, sms, false, 0);
+    const unsigned grid = (unsigned)std::min(m.rows / m.HW * g.tiles, 64LL * sms);
+    const size_t smem = (size_t)(kWarps + 1) * g.lp * 4;
+    if (a.dx) wtconv_norm_planes_long_bwd_kernel<T, true><<<grid, kWarps * 32, smem, s>>>(m, a, d, g);
+    else wtconv_norm_planes_long_bwd_kernel<T, false><<<grid, kWarps * 32, smem, s>>>(m, a, d, g);
 }
 
 }  // namespace

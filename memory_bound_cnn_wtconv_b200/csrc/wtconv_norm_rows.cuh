@@ -16,57 +16,6 @@
 
 namespace wtc {
 
-constexpr int kMaxTeam = 512;      // threads of a CTA-wide team
-constexpr int kTeamThreads = 256;  // threads of a CTA of smaller teams
-
-struct RowsGeom {
-    int tpr, nv, threads, step;  // step: rows a CTA holds at once
-};
-
-// Teams of single channels, for which kernels exist with the width at compile
-// time (the offsets of a thread's slots are then constants): the narrowest that
-// holds a row, since the work for each row weighs more than that for a slot.
-// The last two are CTAs of any width.
-struct SingleTeam {
-    int nv, tpr;
-};
-constexpr SingleTeam kSingles[] = {{4, 8}, {8, 8}, {8, 16}, {8, 32}, {16, 32}, {8, 0}, {16, 0}};
-
-// Chunks: the part of a warp (at least `least` threads, and four: 64 adjacent
-// bytes) that leaves the fewest slots empty, and of those the widest, which
-// holds the fewest registers: 24 slots are 8 x 3, 64 are 32 x 2.  Longer rows
-// take a CTA.  warp: no team wider than a warp.
-inline RowsGeom rows_geom(const MapShape& m, int V, int least, bool warp, int sms) {
-    const int slots = (m.C + V - 1) / V;
-    RowsGeom g{};
-    if (V == 1) {
-        for (const SingleTeam& s : kSingles) {
-            const int tpr = s.tpr ? s.tpr : std::min(kMaxTeam, ((slots + s.nv - 1) / s.nv + 31) / 32 * 32);
-            if (tpr < least || (warp && tpr > 32) || tpr * s.nv < slots) continue;
-            g.tpr = tpr, g.nv = s.nv;
-            break;
-        }
-        if (!g.tpr) g.tpr = warp ? 32 : kMaxTeam;
-    } else {
-        int best = 0;
-        for (int tpr = std::max(4, least); tpr <= 32; tpr *= 2) {
-            const int nv = (slots + tpr - 1) / tpr;
-            if (nv <= 4 && (!best || tpr * nv <= best)) best = tpr * nv, g.tpr = tpr, g.nv = nv;
-        }
-        if (!best) {
-            g.tpr = std::min(kMaxTeam, ((slots + 3) / 4 + 31) / 32 * 32);
-            g.nv = g.tpr * 4 >= slots ? 4 : 0;
-        }
-    }
-    g.threads = g.tpr;
-    if (g.tpr <= 32) {
-        g.threads = kTeamThreads;
-        while (g.threads > 32 && (long long)(g.threads / 2 / g.tpr) * sms >= m.rows) g.threads /= 2;  // few rows: spread them
-    }
-    g.step = g.threads / g.tpr;
-    return g;
-}
-
 // Whether a kernel is for teams within a warp only (CTA-wide ones have four
 // chunks or any number of single channels a thread), so for kTeamThreads.
 template <int V, int NV, int TPR>

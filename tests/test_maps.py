@@ -262,6 +262,23 @@ def test_unaligned_buffers(shape, dtype, layout):
 
 
 @pytest.mark.parametrize("layout", ["nchw", "nhwc"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+def test_unaligned_groups_of_larger_maps(group, dtype, layout):
+    # Enough pixels that the kernels for unaligned buffers put all lanes of a warp along them.
+    shape, gen = (8, 300, 32, 32), gen_of("groups", group, layout)
+    x = make(shape, layout, dtype, gen, shift=1)
+    w = torch.randn(300, generator=gen).cuda()
+    q, scale, _ = wt.rms_norm_q8(x, w, None, EPS, torch.int8, group)
+    v, _ = ref.norm(wide(x), w.double().cpu().numpy(), EPS)
+    tol, s = (301 / 2 + 10) * U, np.repeat(wide(scale), group or 300, axis=1)[:, :300]
+    close(wide(scale), ref.group_max(v, group or 300) / 127.0, tol * wide(scale), "scale")
+    close(wide(q) * s, v, 0.5 * s * (1 + 4 * tol) + 4 * tol * np.abs(v), "q")
+    # the largest value of each group is its top
+    assert (np.concatenate([np.abs(wide(q))[:, k:k + (group or 300)].max(1) for k in range(0, 300, group or 300)]) == 127).all()
+
+
+@pytest.mark.parametrize("layout", ["nchw", "nhwc"])
 def test_infinities_and_nan(layout):
     shape, gen = (2, 24, 4, 8), gen_of("nan", layout)
     x, res = make(shape, layout, F32, gen), make(shape, layout, F32, gen)
