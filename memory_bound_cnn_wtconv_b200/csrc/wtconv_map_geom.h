@@ -58,11 +58,12 @@ struct RowsGeom {
 // Teams of single channels, for which kernels exist with the width at compile
 // time (the offsets of a thread's slots are then constants): the narrowest that
 // holds a row, since the work for each row weighs more than that for a slot.
-// The last two are CTAs of any width.
+// {2, 32} and {4, 32} are left for what needs whole warps (groups of an 8-bit
+// output); the last two are CTAs of any width.
 struct SingleTeam {
     int nv, tpr;
 };
-constexpr SingleTeam kSingles[] = {{4, 8}, {8, 8}, {8, 16}, {8, 32}, {16, 32}, {8, 0}, {16, 0}};
+constexpr SingleTeam kSingles[] = {{4, 8}, {8, 8}, {8, 16}, {2, 32}, {4, 32}, {8, 32}, {16, 32}, {8, 0}, {16, 0}};
 
 // Chunks: the part of a warp (at least `least` threads, and four: 64 adjacent
 // bytes) that leaves the fewest slots empty, and of those the widest, which

@@ -33,6 +33,13 @@ __device__ __forceinline__ float q8_inverse(float scale) {
     return r;
 }
 
+// c >> this is the group of channel c: groups are a power of two of channels, or all of them one.
+__device__ __forceinline__ int group_shift(int group, int groups) { return groups == 1 ? 31 : 31 - __clz(group); }
+
+// A whole number; |v| is 127 and a few units in the last place at most, and a
+// NaN is 0 by the conversion's definition.
+__device__ __forceinline__ uint32_t q8_whole(float v) { return (uint32_t)__float2int_rn(v) & 255; }
+
 // Four values to four bytes.
 __device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d, int q8) {
     if (q8 == WTCONV_E4M3) {
@@ -40,19 +47,12 @@ __device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d,
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
         return lo | hi << 16;
     }
-    const float f[4] = {a, b, c, d};
-    uint32_t r = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int v = isnan(f[i]) ? 0 : max(-127, min(127, __float2int_rn(f[i])));
-        r |= (uint32_t)(v & 255) << (8 * i);
-    }
-    return r;
+    return q8_whole(a) | q8_whole(b) << 8 | q8_whole(c) << 16 | q8_whole(d) << 24;
 }
 
 __device__ __forceinline__ uint8_t q8_one(float v, int q8) {
     if (q8 == WTCONV_E4M3) return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
-    return (uint8_t)(isnan(v) ? 0 : max(-127, min(127, __float2int_rn(v))));
+    return (uint8_t)q8_whole(v);
 }
 
 // |v| as bits that are ordered like |v|, NaN above infinity.

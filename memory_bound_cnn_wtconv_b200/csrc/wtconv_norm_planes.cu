@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
             }
         } else {
             uint32_t* top = reinterpret_cast<uint32_t*>(sums + (warps + 1) * px);
-            const int groups = (m.C + a.group - 1) / a.group;
+            const int groups = (m.C + a.group - 1) / a.group, gs = group_shift(a.group, groups);
             for (int q = threadIdx.x; q < groups * px; q += blockDim.x) top[q] = 0;
             __syncthreads();
 #pragma unroll
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
                 if (now.in(g, 0) && (threadIdx.x & (o - 1) & ~(now.lp() - 1)) == 0) {
 #pragma unroll
                     for (int e = 0; e < VP; ++e)
-                        if (now.has(e)) atomicMax(&top[now.channel(g, 0) / a.group * px + now.pixel(e)], bits[e]);
+                        if (now.has(e)) atomicMax(&top[(now.channel(g, 0) >> gs) * px + now.pixel(e)], bits[e]);
                 }
             }
             __syncthreads();
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
             for (int g = 0; g < G; ++g) {
                 if (!now.in(g, 0)) continue;
                 float inv[VP];
-                now.get(reinterpret_cast<const float*>(top) + now.channel(g, 0) / a.group * px, inv);
+                now.get(reinterpret_cast<const float*>(top) + (now.channel(g, 0) >> gs) * px, inv);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (!now.in(g, j)) continue;

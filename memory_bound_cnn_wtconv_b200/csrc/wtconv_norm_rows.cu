@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThree<V, NV, TPR, JOIN, Q8> ? kTeamThreads : 
                 raw[i] = in(i0 + i) && whole ? *reinterpret_cast<const R*>(x + c) : Chunk<T, V>::zero();
                 if (JOIN != kPlain) rr[i] = in(i0 + i) ? *reinterpret_cast<const R*>(res + c) : Chunk<T, V>::zero();
             }
-            if (JOIN == kDropped) {
+            if constexpr (JOIN == kDropped) {
                 float f[NR][V], r[NR][V];
 #pragma unroll
                 for (int i = 0; i < NR; ++i) unpack(raw[i], f[i]), unpack(rr[i], r[i]);
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThree<V, NV, TPR, JOIN, Q8> ? kTeamThreads : 
                 }
 #pragma unroll
                 for (int i = 0; i < NR; ++i) raw[i] = Chunk<T, V>::from(r[i]);
-            } else if (JOIN == kResidual) {
+            } else if constexpr (JOIN == kResidual) {
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
                     float f[V], r[V];
@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kThree<V, NV, TPR, JOIN, Q8> ? kTeamThreads : 
                 for (int i0 = 0; i0 < iters; i0 += NR) out(i0);
             }
         } else {
-            const int groups = (m.C + a.group - 1) / a.group;
+            const int groups = (m.C + a.group - 1) / a.group, gs = group_shift(a.group, groups);
+            float* scales = a.scale + row * groups;
             float v[NR][V];
             auto values = [&](int i0) {
 #pragma unroll
@@ -154,28 +155,36 @@ __global__ void __launch_bounds__(kThree<V, NV, TPR, JOIN, Q8> ? kTeamThreads : 
                     for (int i = 0; i < NR; ++i) bits = max(bits, largest(i));
                 }
                 scale = q8_scale(team_max(bits, tpr, red), a.q8);
-                if (live && t == 0) a.scale[row] = scale;
+                if (live && t == 0) *scales = scale;
             }
             auto out = [&](int i0) {
                 if (!NV) values(i0);
                 uint32_t bits[NR];
                 if (groups > 1) {
                     // A group is group / V neighbouring slots of a round, a power of two of neighbouring lanes; of single
-                    // channels (teams of one warp) up to four whole rounds.
+                    // channels (teams of one warp) one, two or four whole rounds, each reduced by one instruction
+                    // (118840 rows of 109 bf16 with a residual, groups of 32: 45 us; by five shuffles, in a kernel for
+                    // 256 channels and with a division for each group's address, 113).
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
                         bits[i] = largest(i);
-                        for (int o = min(a.group / V, 32) / 2; o; o >>= 1) bits[i] = max(bits[i], __shfl_xor_sync(0xffffffffu, bits[i], o));
+                        if constexpr (V == 1) {
+                            bits[i] = __reduce_max_sync(0xffffffffu, bits[i]);
+                        } else {
+                            for (int o = a.group / V / 2; o; o >>= 1) bits[i] = max(bits[i], __shfl_xor_sync(0xffffffffu, bits[i], o));
+                        }
                     }
                     if constexpr (V == 1) {
                         if (a.group > 32) {
 #pragma unroll
                             for (int i = 0; i < NR; i += 2) bits[i] = bits[i + 1] = max(bits[i], bits[i + 1]);
                         }
-                        if (a.group > 64) {
+                        if constexpr (NR % 4 == 0) {  // two rounds are at most 64 channels, so one group of more
+                            if (a.group > 64) {
 #pragma unroll
-                            for (int i = 0; i < NR; i += 4)
-                                bits[i] = bits[i + 1] = bits[i + 2] = bits[i + 3] = max(bits[i], bits[i + 2]);
+                                for (int i = 0; i < NR; i += 4)
+                                    bits[i] = bits[i + 1] = bits[i + 2] = bits[i + 3] = max(bits[i], bits[i + 2]);
+                            }
                         }
                     }
                 }
@@ -184,7 +193,7 @@ __global__ void __launch_bounds__(kThree<V, NV, TPR, JOIN, Q8> ? kTeamThreads : 
                     const int c = ((i0 + i) * tpr + t) * V;
                     if (groups > 1) {
                         scale = q8_scale(bits[i], a.q8);
-                        if (in(i0 + i) && (c & (a.group - 1)) == 0) a.scale[row * groups + c / a.group] = scale;
+                        if (in(i0 + i) && (c & (a.group - 1)) == 0) scales[c >> gs] = scale;
                     }
                     if (!in(i0 + i)) continue;
                     float (&f)[V] = v[i];
@@ -224,7 +233,7 @@ void run(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cud
         const unsigned grid = (unsigned)std::min(ctas, ctas <= 2LL * sms ? ctas : (long long)norm_resident(kernel, g.threads, 0) * sms * each);
         kernel<<<grid, g.threads, 0, s>>>(m, a, d, g.tpr, 1.0f / m.C);
     };
-    rows_dispatch<V>(g, [&](auto nv, auto tpr) { go(wtconv_norm_rows_kernel<T, V, nv, tpr, JOIN, Q8>); });
+    rows_dispatch<V, Q8>(g, [&](auto nv, auto tpr) { go(wtconv_norm_rows_kernel<T, V, nv, tpr, JOIN, Q8>); });
 }
 
 template <typename T, int V>

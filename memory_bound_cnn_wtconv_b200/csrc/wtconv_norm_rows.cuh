@@ -22,7 +22,8 @@ template <int V, int NV, int TPR>
 constexpr bool kWithinWarp = NV != 0 && (V > 1 ? NV != 4 : TPR != 0);
 
 // go(nv, tpr) with the geometry's numbers as constants (tpr 0: a runtime one).
-template <int V, typename F>
+// WARP: with the teams that only whole warps need.
+template <int V, bool WARP, typename F>
 void rows_dispatch(const RowsGeom& g, F go) {
     using std::integral_constant;
     constexpr integral_constant<int, 0> any{};
@@ -37,6 +38,10 @@ void rows_dispatch(const RowsGeom& g, F go) {
         if (g.nv == 4 && g.tpr == 8) return go(integral_constant<int, 4>{}, integral_constant<int, 8>{});
         if (g.nv == 8 && g.tpr == 8) return go(integral_constant<int, 8>{}, integral_constant<int, 8>{});
         if (g.nv == 8 && g.tpr == 16) return go(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+        if constexpr (WARP) {
+            if (g.nv == 2 && g.tpr == 32) return go(integral_constant<int, 2>{}, integral_constant<int, 32>{});
+            if (g.nv == 4 && g.tpr == 32) return go(integral_constant<int, 4>{}, integral_constant<int, 32>{});
+        }
         if (g.nv == 8 && g.tpr == 32) return go(integral_constant<int, 8>{}, integral_constant<int, 32>{});
         if (g.nv == 16 && g.tpr == 32) return go(integral_constant<int, 16>{}, integral_constant<int, 32>{});
         if (g.nv == 8) return go(integral_constant<int, 8>{}, any);

@@ -171,7 +171,7 @@ int run(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cuda
     const long long ctas = std::min((m.rows + g.step - 1) / g.step, norm_parts(m, sms));
     const size_t smem = g.nv && g.tpr <= 32 && g.threads > 32 && a.dweight ? (size_t)(g.threads / 32) * m.C * 4 : 0;
     int parts = 0;
-    rows_dispatch<V>(g, [&](auto nv, auto tpr) {
+    rows_dispatch<V, false>(g, [&](auto nv, auto tpr) {
         if (nv == 0 && !a.dres && !a.dx) return;
         auto kernel = wtconv_norm_rows_bwd_kernel<T, V, nv, tpr, DROP>;
         const unsigned grid = (unsigned)std::min(ctas, ctas <= 2LL * sms ? ctas : (long long)norm_resident(kernel, g.threads, smem) * sms);

@@ -40,7 +40,7 @@ static void check_rows(const MapShape& m, int esize, int V, int group) {  // gro
     CHECK(g.step * g.tpr == g.threads && g.step >= 1);
     if (g.nv) {
         CHECK(g.nv * g.tpr >= slots);
-        CHECK(V > 1 ? g.nv <= 4 && (g.tpr <= 32 || g.nv == 4) : g.nv == 4 || g.nv == 8 || g.nv == 16);
+        CHECK(V > 1 ? g.nv <= 4 && (g.tpr <= 32 || g.nv == 4) : g.nv == 4 || g.nv == 8 || g.nv == 16 || (grouped && g.nv == 2));
         if (V == 1 && g.tpr <= 32) {  // a kernel of that width exists
             bool found = false;
             for (const SingleTeam& s : kSingles) found |= s.nv == g.nv && s.tpr == g.tpr;
