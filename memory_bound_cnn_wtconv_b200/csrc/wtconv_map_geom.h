@@ -57,16 +57,18 @@ struct RowsGeom {
 
 // Teams of single channels, for which kernels exist with the width at compile
 // time (the offsets of a thread's slots are then constants): the narrowest that
-// holds a row, since the work for each row weighs more than that for a slot.
+// holds a row, since the work for each row weighs more than that for a slot (11
+// bf16 channels, 64 x 128 x 128, with a residual 29 us by {4, 4}, 39 by {4, 8}).
 // {2, 32} and {4, 32} are left for what needs whole warps (groups of an 8-bit
 // output); the last two are CTAs of any width.
 struct SingleTeam {
     int nv, tpr;
 };
-constexpr SingleTeam kSingles[] = {{4, 8}, {8, 8}, {8, 16}, {2, 32}, {4, 32}, {8, 32}, {16, 32}, {8, 0}, {16, 0}};
+constexpr SingleTeam kSingles[] = {{4, 4}, {4, 8}, {8, 8}, {8, 16}, {2, 32}, {4, 32}, {8, 32}, {16, 32}, {8, 0}, {16, 0}};
 
-// Chunks: the part of a warp (at least `least` threads, and four: 64 adjacent
-// bytes) that leaves the fewest slots empty, and of those the widest, which
+// Chunks: one or two threads for rows of one or two chunks (8 bf16 channels, 64
+// x 128 x 128, with a residual 18 us, 33 with teams of four); else the part of a
+// warp (at least `least` threads, and four: 64 adjacent bytes) that leaves the fewest slots empty, and of those the widest, which
 // holds the fewest registers: 24 slots are 8 x 3, 64 are 32 x 2.  Longer rows
 // take a CTA.  warp: no team wider than a warp.
 inline RowsGeom rows_geom(const MapShape& m, int V, int least, bool warp, int sms) {
@@ -82,7 +84,7 @@ inline RowsGeom rows_geom(const MapShape& m, int V, int least, bool warp, int sm
         if (!g.tpr) g.tpr = warp ? 32 : kMaxTeam;
     } else {
         int best = 0;
-        for (int tpr = std::max(4, least); tpr <= 32; tpr *= 2) {
+        for (int tpr = std::max(slots <= 2 ? slots : 4, least); tpr <= 32; tpr *= 2) {
             const int nv = (slots + tpr - 1) / tpr;
             if (nv <= 4 && (!best || tpr * nv <= best)) best = tpr * nv, g.tpr = tpr, g.nv = nv;
         }

@@ -35,6 +35,7 @@ void rows_dispatch(const RowsGeom& g, F go) {
             case 4: return go(integral_constant<int, 4>{}, any);
         }
     } else {
+        if (g.nv == 4 && g.tpr == 4) return go(integral_constant<int, 4>{}, integral_constant<int, 4>{});
         if (g.nv == 4 && g.tpr == 8) return go(integral_constant<int, 4>{}, integral_constant<int, 8>{});
         if (g.nv == 8 && g.tpr == 8) return go(integral_constant<int, 8>{}, integral_constant<int, 8>{});
         if (g.nv == 8 && g.tpr == 16) return go(integral_constant<int, 8>{}, integral_constant<int, 16>{});

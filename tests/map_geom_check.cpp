@@ -36,7 +36,7 @@ static void check_rows(const MapShape& m, int esize, int V, int group) {  // gro
     const RowsGeom g = rows_geom(m, V, !grouped ? 0 : V == 1 ? 32 : group / V, grouped && V == 1, sms);
     const int slots = (m.C + V - 1) / V;
     CHECK(g.threads >= 32 && g.threads % 32 == 0 && g.threads <= (g.tpr <= 32 ? kTeamThreads : kMaxTeam));
-    CHECK(g.tpr <= 32 ? (g.tpr & (g.tpr - 1)) == 0 && g.tpr >= 4 : g.tpr % 32 == 0 && g.threads == g.tpr);
+    CHECK(g.tpr <= 32 ? (g.tpr & (g.tpr - 1)) == 0 && g.tpr >= (V == 1 ? 4 : std::min(slots, 4)) : g.tpr % 32 == 0 && g.threads == g.tpr);
     CHECK(g.step * g.tpr == g.threads && g.step >= 1);
     if (g.nv) {
         CHECK(g.nv * g.tpr >= slots);
