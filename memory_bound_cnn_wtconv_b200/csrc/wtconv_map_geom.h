@@ -68,10 +68,13 @@ constexpr SingleTeam kSingles[] = {{4, 4}, {4, 8}, {8, 8}, {8, 16}, {2, 32}, {4,
 
 // Chunks: one or two threads for rows of one or two chunks (8 bf16 channels, 64
 // x 128 x 128, with a residual 18 us, 33 with teams of four); else the part of a
-// warp (at least `least` threads, and four: 64 adjacent bytes) that leaves the fewest slots empty, and of those the widest, which
-// holds the fewest registers: 24 slots are 8 x 3, 64 are 32 x 2.  Longer rows
-// take a CTA.  warp: no team wider than a warp.
-inline RowsGeom rows_geom(const MapShape& m, int V, int least, bool warp, int sms) {
+// warp (at least `least` threads, and four: 64 adjacent bytes) that leaves the
+// fewest slots empty, and of those the widest, which holds the fewest
+// registers: 24 slots are 8 x 3, 64 are 32 x 2.  pairs: but two slots a thread
+// rather than one, for the work around each row (256 bf16 channels, 131072 rows,
+// residual: e4m3 45 us, 53 with 32 x 1, element dropout 55 and 61; but the
+// backward of 128 fp32 54 and 52).  Longer rows take a CTA.  warp: no team wider than a warp.
+inline RowsGeom rows_geom(const MapShape& m, int V, int least, bool warp, bool pairs, int sms) {
     const int slots = (m.C + V - 1) / V;
     RowsGeom g{};
     if (V == 1) {
@@ -86,7 +89,8 @@ inline RowsGeom rows_geom(const MapShape& m, int V, int least, bool warp, int sm
         int best = 0;
         for (int tpr = std::max(slots <= 2 ? slots : 4, least); tpr <= 32; tpr *= 2) {
             const int nv = (slots + tpr - 1) / tpr;
-            if (nv <= 4 && (!best || tpr * nv <= best)) best = tpr * nv, g.tpr = tpr, g.nv = nv;
+            if (nv > 4 || (best && tpr * nv > best) || (pairs && tpr * nv == best && g.nv <= 2)) continue;
+            best = tpr * nv, g.tpr = tpr, g.nv = nv;
         }
         if (!best) {
             g.tpr = std::min(kMaxTeam, ((slots + 3) / 4 + 31) / 32 * 32);

@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[g][j] = now.channel(g, j) < m.C ? a.weight[now.channel(g, j)] : 0.0f;
     }
+    const int groups = Q8 ? (m.C + a.group - 1) / a.group : 0, gs = Q8 ? group_shift(a.group, groups) : 0;
     next.at(blockIdx.x);
     fetch(next, 0);
     int stage = 0;
@@ -124,7 +125,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_kernel(MapS
             }
         } else {
             uint32_t* top = reinterpret_cast<uint32_t*>(sums + (warps + 1) * px);
-            const int groups = (m.C + a.group - 1) / a.group, gs = group_shift(a.group, groups);
             for (int q = threadIdx.x; q < groups * px; q += blockDim.x) top[q] = 0;
             __syncthreads();
 #pragma unroll

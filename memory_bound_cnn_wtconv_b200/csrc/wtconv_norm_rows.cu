@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(kThree<V, NV, TPR, JOIN, Q8> ? kTeamThreads : 
             if (i * tpr + t < slots) load_weight<V>(a.weight + (i * tpr + t) * V, w[i]);
         }
     }
+    const int groups = Q8 ? (m.C + a.group - 1) / a.group : 0, gs = Q8 ? group_shift(a.group, groups) : 0;
     // Every thread of a CTA makes the same number of rounds.
     for (long long row0 = (long long)blockIdx.x * step; row0 < m.rows; row0 += (long long)gridDim.x * step) {
         const long long row = row0 + threadIdx.x / tpr;
@@ -132,7 +133,6 @@ __global__ void __launch_bounds__(kThree<V, NV, TPR, JOIN, Q8> ? kTeamThreads : 
                 for (int i0 = 0; i0 < iters; i0 += NR) out(i0);
             }
         } else {
-            const int groups = (m.C + a.group - 1) / a.group, gs = group_shift(a.group, groups);
             float* scales = a.scale + row * groups;
             float v[NR][V];
             auto values = [&](int i0) {
@@ -223,7 +223,7 @@ void run(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms, cud
     // With groups, what makes a round of slots whole groups (single channels: a warp, to which a group is whole rounds
     // or a part of one).
     const bool grouped = Q8 && a.group < m.C;
-    const RowsGeom g = rows_geom(m, V, !grouped ? 0 : V == 1 ? 32 : a.group / V, grouped && V == 1, sms);
+    const RowsGeom g = rows_geom(m, V, !grouped ? 0 : V == 1 ? 32 : a.group / V, grouped && V == 1, true, sms);
     const long long ctas = (m.rows + g.step - 1) / g.step;
     // Several CTAs one after another to each place on an SM, so that their loads and stores overlap other CTAs', unless
     // what a thread computes weighs more than the memory (512 channels, 32 x 64 x 64, one, two and eight: fp32 with a

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThree<V, NV, TPR> ? kTeamThreads : kMaxTeam, 
 // The number of partial vectors, or 0 if there are none (NV = 0).
 template <typename T, int V, bool DROP>
 int run(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
-    const RowsGeom g = rows_geom(m, V, 0, false, sms);
+    const RowsGeom g = rows_geom(m, V, 0, false, false, sms);
     const long long ctas = std::min((m.rows + g.step - 1) / g.step, norm_parts(m, sms));
     const size_t smem = g.nv && g.tpr <= 32 && g.threads > 32 && a.dweight ? (size_t)(g.threads / 32) * m.C * 4 : 0;
     int parts = 0;

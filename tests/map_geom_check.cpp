@@ -31,9 +31,9 @@ static void check_divide(const MapShape& m, long long d, long long most) {
         if (n >= 0 && n <= most) CHECK(v(n) == n / d);
 }
 
-static void check_rows(const MapShape& m, int esize, int V, int group) {  // group 0: no 8-bit output or one group
+static void check_rows(const MapShape& m, int esize, int V, int group, bool pairs) {  // group 0: no 8-bit output or one group
     const bool grouped = group > 0 && group < m.C;
-    const RowsGeom g = rows_geom(m, V, !grouped ? 0 : V == 1 ? 32 : group / V, grouped && V == 1, sms);
+    const RowsGeom g = rows_geom(m, V, !grouped ? 0 : V == 1 ? 32 : group / V, grouped && V == 1, pairs, sms);
     const int slots = (m.C + V - 1) / V;
     CHECK(g.threads >= 32 && g.threads % 32 == 0 && g.threads <= (g.tpr <= 32 ? kTeamThreads : kMaxTeam));
     CHECK(g.tpr <= 32 ? (g.tpr & (g.tpr - 1)) == 0 && g.tpr >= (V == 1 ? 4 : std::min(slots, 4)) : g.tpr % 32 == 0 && g.threads == g.tpr);
@@ -161,8 +161,10 @@ int main(int argc, char** argv) {
     for (int esize : {4, 2}) {
         const int V = 16 / esize;
         for (int group : {0, 32, 64, 128}) {
-            if (C % V == 0) check_rows(m, esize, V, group);
-            check_rows(m, esize, 1, group);
+            for (bool pairs : {false, true}) {
+                if (C % V == 0) check_rows(m, esize, V, group, pairs);
+                check_rows(m, esize, 1, group, pairs);
+            }
             for (int tensors = 1; tensors <= 3; ++tensors) {
                 const int clipped = group == 0 || group > C ? C : group;  // as the calls do
                 for (int q : {0, clipped}) {
