@@ -238,6 +238,25 @@ def test_few_and_many_rows(rows):
         check_backward(h, dy, None, w, None, *wt.rms_norm_backward(h, dy, w, rstd))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("C", [1, 3, 4, 5, 8, 12, 16, 17])
+def test_narrow_rows(C, dtype):
+    # Rows of one or two chunks, or of few single channels: a thread or a few own one, and CTAs walk many of them.
+    shape, layout = (2, C, 181, 211), "nhwc"
+    gen = gen_of("narrow", C, dtype)
+    x, res, dy = (make(shape, layout, dtype, gen) for _ in range(3))
+    w = torch.randn(C, generator=gen).cuda()
+    drop = wt.Drop(0.4, "element", C, 3)
+    y, h, rstd = wt.rms_norm_forward(x, w, res, drop, EPS)
+    check_forward(x, res, w, drop, y, h, rstd)
+    check_backward(h, dy, res, w, drop, *wt.rms_norm_backward(h, dy, w, rstd, res, drop))
+    v, _ = ref.norm(wide(h), w.double().cpu().numpy(), EPS)
+    q, scale, _ = wt.rms_norm_q8(h, w, None, EPS, torch.int8)
+    tol, s = ((C + 1) / 2 + 10) * U, np.repeat(wide(scale), C, axis=1)
+    close(wide(scale), np.maximum(ref.group_max(v, C) / 127.0, 2.0 ** -126), tol * wide(scale), "scale")
+    close(wide(q) * s, v, 0.5 * s * (1 + 4 * tol) + 4 * tol * np.abs(v), "q")
+
+
 @pytest.mark.parametrize("layout", ["nchw", "nhwc"])
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(2, 96, 8, 8), (1, 40, 16, 4), (1, 1024, 4, 4)], ids=str)
