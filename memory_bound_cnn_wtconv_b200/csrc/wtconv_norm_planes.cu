@@ -191,7 +191,7 @@ bool run_fwd(const MapShape& m, const NormFwdArgs& a, const MapDrop& d, int sms,
     const size_t smem = g.head + (size_t)planes_sums(g, VP, groups) * 4;
     if (smem > kMostSmem) return false;
     planes_dispatch<RAG>(g, [&](auto rag, auto quads) {
-        return launch(wtconv_norm_planes_kernel<T, VP, rag, quads, JOIN, Q8>, m, a, d, g, smem, 1LL << 30, sms, s);
+        return launch<wtconv_norm_planes_kernel<T, VP, rag, quads, JOIN, Q8>>(m, a, d, g, smem, 1LL << 30, sms, s);
     });
     return true;
 }

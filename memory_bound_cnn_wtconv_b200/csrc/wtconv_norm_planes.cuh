@@ -23,6 +23,7 @@
 // its registers for all its tiles.
 #pragma once
 
+#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 
@@ -250,12 +251,29 @@ int planes_dispatch(const PlanesGeom& g, F go) {
     return g.iters == 1 ? go(rag, one) : go(rag, two);
 }
 
+// Lets a kernel have the shared memory that any call asks for, once per kernel
+// and device.  The limit belongs to the kernel, not to a call: set to each
+// call's own size it would fall below what a call on another host thread is
+// about to launch with.  Threads that meet in the first call set the same value.
+template <auto kernel>
+cudaError_t opt_in_smem() {
+    static std::atomic<bool> done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const bool known = dev >= 0 && dev < 64;
+    if (e != cudaSuccess || (known && done[dev].load(std::memory_order_acquire))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
+    if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
 // Launches a kernel on at most `most` CTAs, as many as the SMs hold at once.
-template <typename K, typename A>
-int launch(K kernel, const MapShape& m, const A& a, const MapDrop& d, const PlanesGeom& g, size_t smem, long long most, int sms, cudaStream_t s) {
+// An error is left for the caller's cudaGetLastError().
+template <auto kernel, typename A>
+int launch(const MapShape& m, const A& a, const MapDrop& d, const PlanesGeom& g, size_t smem, long long most, int sms, cudaStream_t s) {
     const int threads = g.warps * 32;
     long long ctas = std::min(m.rows / m.HW * g.tiles, most);
-    if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 * 1024 && opt_in_smem<kernel>() != cudaSuccess) return 1;
     if (ctas > sms) ctas = std::min(ctas, (long long)norm_resident(kernel, threads, smem) * sms);
     kernel<<<(unsigned)ctas, threads, smem, s>>>(m, a, d, g);
     return (int)ctas;

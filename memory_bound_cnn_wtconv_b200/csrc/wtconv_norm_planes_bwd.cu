@@ -130,9 +130,9 @@ int run_bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, 
     const size_t smem = g.head + (size_t)planes_sums(g, VP, 0) * 4;
     const long long most = norm_parts(m, sms);
     return planes_dispatch<RAG>(g, [&](auto rag, auto quads) {
-        if (dh == kNone) return launch(wtconv_norm_planes_bwd_kernel<T, VP, rag, quads, DROP, kNone>, m, a, d, g, smem, most, sms, s);
-        if (dh == kStaged) return launch(wtconv_norm_planes_bwd_kernel<T, VP, rag, quads, DROP, kStaged>, m, a, d, g, smem, most, sms, s);
-        return launch(wtconv_norm_planes_bwd_kernel<T, VP, rag, quads, DROP, kDirect>, m, a, d, g, smem, most, sms, s);
+        if (dh == kNone) return launch<wtconv_norm_planes_bwd_kernel<T, VP, rag, quads, DROP, kNone>>(m, a, d, g, smem, most, sms, s);
+        if (dh == kStaged) return launch<wtconv_norm_planes_bwd_kernel<T, VP, rag, quads, DROP, kStaged>>(m, a, d, g, smem, most, sms, s);
+        return launch<wtconv_norm_planes_bwd_kernel<T, VP, rag, quads, DROP, kDirect>>(m, a, d, g, smem, most, sms, s);
     });
 }
 
