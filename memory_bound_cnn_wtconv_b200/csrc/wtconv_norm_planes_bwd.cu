@@ -69,9 +69,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
         tile_sum<VP>(now, gh, sums, [&](int, float s) { return s * geom.per_channel; });
         bool whole = true;
         if (DROP && d.mode == WTCONV_DROP_SAMPLE) whole = keep_sample(d, offset, now.b);
-        // dres = dh + (r * w) * dy - (r^3 mean(g * h)) * h
+        // dres = dh + r * (w * dy - (r^2 mean(g * h)) * h), factor by factor: r^3 is no float32 number for r above 7e12
+        // or, with all its bits, below 2e-13
 #pragma unroll
-        for (int e = 0; e < VP; ++e) gh[e] *= -(r[e] * r[e] * r[e]);
+        for (int e = 0; e < VP; ++e) gh[e] = -(gh[e] * r[e]) * r[e];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float fe[4][VP] = {};
@@ -84,8 +85,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
                 if (DH == kStaged) now.load(stage, NT, 2, g, j, fe[j]);
                 if (DH == kDirect && now.in(g, j)) now.load(a.dh, g, j, fe[j]);
                 mul_n(fg, w[g][j]);
+                fma_n(fh, gh, fg);
                 fma_n(fg, r, fe[j]);
-                fma_n(fh, gh, fe[j]);
                 if (a.dres && now.in(g, j)) now.store(a.dres, g, j, fe[j]);
             }
             if (DROP && a.dx) {
