@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(kThree<V, NV, TPR> ? kTeamThreads : kMaxTeam, 
         }
         if (!a.dres && !(DROP && a.dx)) continue;
         gh = team_sum(gh, tpr, red);
-        const float s = -(gh * per_channel) * r * r * r;  // dres = dh + (r * w) * dy + s * h
+        // dres = dh + r * (w * dy + s * h): r^3 mean(g * h) may leave float32 where the gradient does not
+        const float s = -(gh * per_channel) * r * r;
         auto out = [&](int i0) {
             if (!NV) load(i0), load_dh(i0);
             float fe[NR][V];
@@ -111,8 +112,8 @@ __global__ void __launch_bounds__(kThree<V, NV, TPR> ? kTeamThreads : kMaxTeam, 
                 unpack(gr[i], fg);
                 if (!kHold) load_weight<V>(a.weight + c, w[i]);
                 mul_n(fg, w[i]);
+                fma_n(fh, s, fg);
                 fma_n(fg, r, fe[i]);
-                fma_n(fh, s, fe[i]);
                 if (a.dres && in(i0 + i)) *reinterpret_cast<R*>(static_cast<T*>(a.dres) + base + c) = Chunk<T, V>::from(fe[i]);
             }
             if (DROP && a.dx) {

@@ -12,6 +12,8 @@ pytestmark = pytest.mark.gpu
 # ordinary sizes.  Planes of whole chunks, of half chunks (in bf16, in fp32), ragged ones, buffers off their alignment, and
 # many channels.
 PLANES = [((2, 12, 4, 8), 0), ((2, 12, 3, 4), 0), ((2, 12, 3, 6), 0), ((2, 13, 3, 5), 0), ((2, 12, 4, 8), 1), ((1, 300, 3, 5), 0)]
+# Chunks, single channels, rows of a CTA, and rows longer than its registers.
+ROWS = [(9, 16, 1, 1), (9, 11, 1, 1), (3, 1200, 1, 1), (3, 1201, 1, 1), (2, 16400, 1, 1), (2, 16401, 1, 1)]
 
 
 def check(shape, layout, dtype, size, dsize, eps, shift=0):
@@ -34,3 +36,11 @@ def check(shape, layout, dtype, size, dsize, eps, shift=0):
                                             (1e-15, 1e10, 1e-36)], ids=str)
 def test_planes(shape, shift, size, dsize, eps, dtype):
     check(shape, "nchw", dtype, size, dsize, eps, shift)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", ROWS, ids=str)
+@pytest.mark.parametrize("size,dsize,eps", [(0.0, 1.0, 1e-28), (1e14, 1.0, 1e-6), (1e16, 1.0, 1e-6), (1e17, 1e-8, 1e-6),
+                                            (1e-15, 1e10, 1e-36)], ids=str)
+def test_rows(shape, size, dsize, eps, dtype):
+    check(shape, "rows", dtype, size, dsize, eps)
