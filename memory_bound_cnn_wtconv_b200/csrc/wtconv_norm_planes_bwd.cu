@@ -84,9 +84,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
                 now.load(stage, NT, 1, g, j, fg);
                 if (DH == kStaged) now.load(stage, NT, 2, g, j, fe[j]);
                 if (DH == kDirect && now.in(g, j)) now.load(a.dh, g, j, fe[j]);
-                mul_n(fg, w[g][j]);
-                fma_n(fh, gh, fg);
-                fma_n(fg, r, fe[j]);
+                mul_n(fh, gh);
+                fma_n(fg, w[g][j], fh);
+                fma_n(fh, r, fe[j]);
                 if (a.dres && now.in(g, j)) now.store(a.dres, g, j, fe[j]);
             }
             if (DROP && a.dx) {
