@@ -6,7 +6,8 @@ calls marshal arguments for the C ABI in ``include/wtconv.h``, which has the
 formulas.  Activations are [B, C, H, W] maps, contiguous (NCHW) or
 channels-last contiguous (NHWC), or contiguous [N, C] rows, in float32 or
 bfloat16 on one CUDA device; the activations of a call share shape, layout and
-type.  Any size is taken, odd ones and B = 0 too.
+type.  Any size is taken, odd ones and B = 0 too, up to extents of 2^31 - 1,
+2^30 pixels of a plane and 2^24 channels.
 
 A call runs on ``stream`` if given (what it allocates then belongs to that
 stream), else on the current stream of the activations' device.  Calls that may
@@ -32,6 +33,7 @@ __all__ = [
 _MODES = {"element": 0, "channel": 1, "sample": 2}
 _Q8 = {torch.float8_e4m3fn: 0, torch.int8: 1}
 _M64 = (1 << 64) - 1
+_MOST = (1 << 31) - 1  # of the descriptor's C ints
 
 
 class MapDesc(ctypes.Structure):
@@ -104,6 +106,8 @@ class _Map:
     __slots__ = ("desc", "ref", "C", "layout", "flat", "rows")
 
     def __init__(self, shape, dtype, layout: int):
+        if max(shape) > _MOST:  # ctypes would pass it modulo 2^32
+            raise ValueError(f"an extent is over {_MOST}: {tuple(shape)}")
         B, C, H, W = shape if len(shape) == 4 else (*shape, 1, 1)
         self.desc = MapDesc(B, C, H, W, F32 if dtype is torch.float32 else BF16, layout)
         self.ref = ctypes.byref(self.desc)
