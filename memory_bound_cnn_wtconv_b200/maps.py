@@ -490,7 +490,7 @@ class BranchDropout(torch.nn.Module):
         super().__init__()
         Drop(p, mode)  # raises for what is out of range
         self.p, self.mode, self.capturable = float(p), mode, bool(capturable)
-        self.seed = int(torch.randint(1 << 62, (1,))) if seed is None else int(seed)
+        self.seed = int(torch.randint(1 << 62, (1,), device="cpu")) if seed is None else int(seed)
         self.steps = 0
         if self.capturable:
             self.register_buffer("step", torch.zeros((1,), dtype=torch.int64, device=device))
