@@ -309,8 +309,12 @@ typedef enum { WTCONV_E4M3 = 0, WTCONV_I8 = 1 } wtconv_q8_t;
 /* wtconv_rms_norm_forward with an 8-bit output.  v = h * rstd * weight stays in
  * float32; each group of `group` adjacent channels of a row (32, 64 or 128, the
  * last may be short; 0: all C) has
- *   scale = max(max |v| / top, 2^-126),  q = v / scale to nearest, ties to even, top = 448 or 127;
- * a NaN or infinity in h makes every scale and q of its row what the formulas
+ *   scale = max(max |v| / top, 2^-126),  q = v / scale to nearest, ties to even, top = 448 or 127.
+ * Both in float32: the scale is off by at most 2^-23 of it (a product with the
+ * float32 number next to 1 / top), and v / scale by at most 3 * 2^-24 of it (a
+ * product with a reciprocal) before its rounding to 8 bits, so a quotient that
+ * close to a tie may go to either neighbour.
+ * A NaN or infinity in h makes every scale and q of its row what the formulas
  * give (a NaN scale's e4m3 are NaN, its whole numbers 0).
  * q: one byte an element in x's layout.  scale: float32, a B x groups x H x W
  * map in x's layout.  residual and h as above. */
