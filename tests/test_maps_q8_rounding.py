@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import memory_bound_cnn_wtconv_b200 as wt
-from test_maps import EPS, F32, U, close, gen_of, make, wide
+import map_reference as ref
+from test_maps import BF16, EPS, F32, U, check_forward, close, gen_of, make, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,31 @@ def test_values_next_to_a_tie():
             q = wt.rms_norm_q8(row, torch.ones(8, device="cuda"), dtype=kind)[0].float()[0, 1:5].tolist()
             for got, m in zip(q, mids):
                 assert (got - m) * side > 0, (kind, m, side, got)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["nchw", "nhwc"])
+@pytest.mark.parametrize("shape", [(2, 96, 8, 8), (1, 40, 16, 4), (3, 130, 9, 7), (1, 1024, 4, 4)], ids=str)
+def test_unaligned_buffers(shape, layout, dtype):
+    # One element off, both 8-bit types, with and without a residual: every value of q, scale and h.
+    gen = gen_of("unaligned q8", shape, layout)
+    x, res = make(shape, layout, dtype, gen, shift=1), make(shape, layout, dtype, gen, shift=1)
+    C = shape[1]
+    w = torch.randn(C + 1, generator=gen).cuda()[1:]
+    tol = ((C + 1) / 2 + 10) * U
+    for residual in (None, res):
+        for kind, top in TOPS.items():
+            for group in (0, 32, 64, 128):
+                q = torch.empty(x.numel() + 1, dtype=torch.int8, device="cuda")[1:].view(kind).as_strided(x.shape, x.stride())
+                q, scale, h = wt.rms_norm_q8(x, w, residual, EPS, kind, group, q=q)
+                if residual is None:
+                    assert h is x
+                else:
+                    assert torch.equal(h, wt.rms_norm_forward(x, w, residual, eps=EPS)[1])
+                    check_forward(x, residual, w, None, *wt.rms_norm_forward(x, w, residual, eps=EPS))
+                v, _ = ref.norm(wide(h), w.double().cpu().numpy(), EPS)
+                want = np.maximum(ref.group_max(v, group or C) / top, 2.0 ** -126)
+                close(wide(scale), want, tol * want, "scale")
+                s = np.repeat(wide(scale), group or C, axis=1)[:, :C]
+                t = v / s
+                close(wide(q.float()), t, half_step(t, kind) * (1 + 4 * tol) + 4 * tol * np.abs(t), "q")
