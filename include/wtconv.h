@@ -240,7 +240,8 @@ wtconv_status_t wtconv_backward_weight_noalloc(const wtconv_desc_t *d, const voi
  *   - Outputs overlap neither an input nor another output (WTCONV_ERR_ARGUMENT).
  *   - Results do not depend on the order in which CTAs run: repeated calls
  *     return the same bits.
- *   - Arithmetic is float32.
+ *   - Arithmetic is float32.  So are sums: a row whose squares add up past
+ *     float32's range has rstd 0, and with it y 0.
  *   - Calls that may run at the same time need workspaces of their own.
  * ------------------------------------------------------------------------ */
 typedef struct {
@@ -259,7 +260,9 @@ typedef enum { WTCONV_DROP_ELEMENT = 0, WTCONV_DROP_CHANNEL = 1, WTCONV_DROP_SAM
  *   counter = (c / 4, r mod 2^32, r / 2^32, (offset + *offset_dev) mod 2^32),
  * r the row (ELEMENT) or the sample b (CHANNEL; SAMPLE with c = 0).  Channel c
  * takes word c mod 4 and is dropped where it is below floor(p * 2^32).  So the
- * mask depends on neither layout nor type.  A dropped element counts as 0,
+ * mask depends on neither layout nor type.  Rows and samples count from 0 in
+ * each call, so processes that share a batch out need a seed each, or they drop
+ * the same places of different samples.  A dropped element counts as 0,
  * whatever it holds; the others grow by the float32 number next to 1/(1-p). */
 typedef struct {
     double p;                   /* 0 <= p < 1 */

@@ -50,7 +50,9 @@ class Drop:
     """One call's dropout: probability ``p`` (0 <= p < 1), what a decision
     covers (``mode``: "element", "channel" of a sample, or "sample"), and the
     counter that names the mask: the same ``seed`` and ``offset`` give the same
-    mask, in both layouts and types and in the backward.
+    mask, in both layouts and types and in the backward.  Processes that share a
+    batch out need a seed each: a call's rows and samples count from 0, so the
+    same seed would drop the same places of different samples.
 
     ``offset`` is a number (of the step, say), or an int64 CUDA tensor of one
     element, which the kernels read when they run: a captured graph that moves
@@ -477,7 +479,9 @@ class BranchDropout(torch.nn.Module):
     training, and plainly residual + x in evaluation.
 
     ``seed`` names the module's masks (drawn from torch's CPU generator if not
-    given, so processes that seed it alike draw alike); each training call takes
+    given).  Data-parallel processes that seed alike drop the same places of
+    their shares: give each a seed of its own, such as one number plus the rank,
+    and again after loading a state that they share.  Each training call takes
     the next step as its offset.  ``next_drop()`` is that call's ``Drop``, for a
     fused norm.  With ``capturable`` the step is a CUDA tensor which the calls
     move on, so every replay of a captured graph draws new masks.  Seed and
