@@ -106,7 +106,7 @@ KERNEL_SOURCES = ("wtconv_kernels.cuh", "wtconv_kinst.cuh", "wtconv_plan.h", "wt
                   "wtconv_launch.h", "wtconv_api.cu", "wtconv_k1.cu", "wtconv_k3.cu", "wtconv_k5.cu", "wtconv_k7.cu")
 MEASURED_TRAFFIC = {
     # (workload, call): (bytes per launch, kernel, source digest, profile)
-    ("stage1", "bwd_w"): (79442176.0, "wtconv_bwdw_partial_kernel",
+    ("stage1", "bwd_w"): (79220992.0, "wtconv_bwdw_partial_kernel",
                           "e56de9a329b11ff1774ddc61f2ae5b0193e2cf6322440330291aab5bf2427993",
                           "profiles/wtconv_bwdw_partial_kernel_stage1.md"),
 }
