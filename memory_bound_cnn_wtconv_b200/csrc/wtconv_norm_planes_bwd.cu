@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) wtconv_norm_planes_bwd_kernel(
 template <typename T, int VP, int RAG, bool DROP>
 int run_bwd(const MapShape& m, const NormBwdArgs& a, const MapDrop& d, int sms, cudaStream_t s) {
     PlanesGeom g;
-    // dh is staged unless that takes a tile below 64 bytes of a plane (768 channels, 128 x 7 x 7 fp32: 142 us with it, 81
+    // dh is staged unless that takes a tile below 64 bytes of a plane (768 channels, 128 x 7 x 7 fp32: 142 us with it, 79
     // without).
     int dh = !a.dh ? kNone : kStaged;
     if (!a.dh || !planes_geom(m, VP, RAG, sizeof(T), 3, &g) || g.lp * VP * (int)sizeof(T) < std::min(64, m.HW * (int)sizeof(T))) {
